@@ -74,7 +74,7 @@ def draw(rng):
     if op == "rope":
         dtype = rng.choice(["bf16", "bf16", "fp32"])
         return dict(op=op, T=_log(rng, 1, 8192 if dtype == "bf16" else 4096), Hkv=rng.choice([1, 2, 4, 8]),
-                    G=rng.choice([1, 2, 3, 4, 4]), page=page, dtype=dtype, rot=rng.choice([128, 128, 64, 32, 96, 6]),
+                    G=rng.choice([1, 2, 3, 4, 4]), page=page, dtype=dtype, rot=rng.choice([128, 128, 64, 32, 96, 16]),
                     pairs=rng.choice(["halves", "neighbours"]), norm=rng.random() < 0.7, far=_log(rng, 10000, 500000), mix=mix)
     Hkv = rng.choice([1, 2, 4, 8])
     if op == "gather":
