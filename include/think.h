@@ -14,7 +14,9 @@
  *   think_compact_keys        K'[n,t] = K[n, idx[t]]   (V is not touched)
  *   think_pruned_decode_attn  out = softmax((q[idx] . K'^T) / sqrt(d)) V
  *
- * plus think_prune, the first three in two launches; think_append_keys,
+ * and, before them, the paged cache that a batch of prompts grows in
+ * (think_extend_pages, think_norm_rope_append, think_paged_attn,
+ * think_gather_pages).  Further: think_prune, the first three in two launches; think_append_keys,
  * which appends new tokens' keys to the thinner cache; a 4-bit thinner
  * cache (think_quantize_keys_q4, think_pruned_decode_attn_q4); a kept
  * width per head (think_select_adaptive, think_prune_adaptive and the _ragged
@@ -81,6 +83,9 @@ typedef enum { THINK_F32 = 0, THINK_BF16 = 1 } think_dtype_t;
 #define THINK_DEVICE_TIMEOUT_READY   0x4u   /* a head's channel selection never became ready */
 #define THINK_DEVICE_TIMEOUT_BARRIER 0x8u   /* a block-internal barrier was not reached */
 #define THINK_DEVICE_OOB             0x10u  /* debug builds only: an index check failed (store skipped) */
+/* Written by the paged calls (not a timeout: the call's other outputs are valid, see there). */
+#define THINK_DEVICE_NO_PAGES        0x20u  /* a request got no room: free pages, table row or row arrays ran out */
+#define THINK_DEVICE_BAD_PAGE        0x40u  /* a page that a call needs lies outside the pool */
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char *think_status_string(think_status_t status);
@@ -373,6 +378,120 @@ think_status_t think_select_tokens(const float *mass, int B, int Hkv, int64_t N,
  * an out-of-range index gives a zero row).  One launch. */
 think_status_t think_gather_tokens(const void *x, const int64_t x_strides[3], int B, int Hkv, int64_t N, int d,
                                    think_dtype_t dtype, const int32_t *kept, int M, void *out, void *stream);
+
+/* ------------------------------------------------------- paged cache --
+ * The prompt side of the cache: requests of different lengths grow K and V in
+ * pages, their new tokens attend over the pages, and a finished prompt is
+ * handed to the channel pruning.  One step of a layer:
+ *     think_extend_pages      lengths -> block tables, positions, slots (once a step)
+ *     think_norm_rope_append  norm and rotate q and k, write k and v at the slots
+ *     think_paged_attn        the new tokens attend over their requests' pages
+ * and before pruning a request
+ *     think_gather_pages      its pages -> contiguous K (and V) for think_prune.
+ *
+ * Layout.  A pool of num_pages pages of page_size rows (a multiple of 16)
+ * holds the keys, another the values: the row of page p, head h and row i lies
+ * at cache + p*strides[0] + h*strides[1] + i*strides[2], its 128 channels
+ * contiguous.  Pages may be [page][head][row][128] or [page][row][head][128] or
+ * any other strides that are multiples of 16 bytes.  Position n of request b
+ * lies in page block_table[b*table_ld + n / page_size], row n % page_size; its
+ * slot is page * page_size + row.  max_blocks entries of a table row may be
+ * used (table_ld >= max_blocks); max_blocks * page_size <= 2^30.  The new tokens
+ * of all requests lie one after another in T rows: request b has the rows
+ * q_start[b] .. q_start[b+1] - 1.  Lengths, tables and row ranges are DEVICE
+ * arrays and are read when the kernels run, so that a captured call follows
+ * the lengths of each replay.  What they hold is checked on the device: no
+ * call reads or writes outside its buffers whatever they hold (lengths are
+ * held to [0, max_blocks * page_size], row ranges to [0, T]).
+ *
+ * think_extend_pages: one launch.  Request b, with kv_lens[b] tokens cached,
+ * gets new_lens[b] (>= 0; less counts as 0) new tokens:
+ *     q_start      running sums of new_lens (held to T), [B + 1]
+ *     kv_lens_out  kv_lens[b] + new_lens[b]
+ *     positions    [T] kv_lens[b] + i for its i-th new token (int32)
+ *     slots        [T] the slot of that position (int64)
+ * and rows of T behind the last request get position 0 and slot -1.  Pages
+ * that the new tokens begin are taken from the stack free_pages[0 ..
+ * *free_count - 1], of n_free entries, from its top, in the order of requests
+ * and positions, and written to the block table (other entries are left as
+ * they are); *free_count_out is what remains.  To give pages back, write them
+ * at free_pages[*free_count ..] and raise *free_count.
+ *   A request gets no pages, keeps its length and has slots -1, with
+ * THINK_DEVICE_NO_PAGES in the status word, if its tokens do not fit its table
+ * row or the T rows, or if the pages wanted by it and the requests before it
+ * (those that fit) exceed *free_count.  The slot of a page number below 0
+ * (in the table or the stack) is -1, with THINK_DEVICE_BAD_PAGE.
+ *   kv_lens_out may be kv_lens and free_count_out may be free_count; no other
+ * buffers may overlap.  workspace: think_extend_pages_workspace_size() bytes,
+ * zeroed once (think_workspace_init); it holds the status word. */
+size_t think_extend_pages_workspace_size(void);
+think_status_t think_extend_pages(const int32_t *new_lens, const int32_t *kv_lens, int B, int page_size,
+                                  int32_t *block_table, int64_t table_ld, int max_blocks, const int32_t *free_pages,
+                                  int n_free, const int32_t *free_count, int64_t T, int32_t *kv_lens_out,
+                                  int32_t *free_count_out, int32_t *q_start, int32_t *positions, int64_t *slots,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+/* think_norm_rope_append: one launch.  For each token t and head row x of q
+ * and k (fp32 arithmetic, one rounding to dtype at the end):
+ *     x  <- x * rsqrt(mean(x^2) + eps) * weight      (if the weight is given)
+ *     (x1, x2) <- (x1 cos a - x2 sin a, x2 cos a + x1 sin a),
+ *                 a = positions[t] * inv_freq[i] (fp64), i = 0 .. rot/2 - 1,
+ * where pair i is channels (i, i + rot/2), or (2i, 2i + 1) if `neighbours` is
+ * not 0; channels from rot on are not turned.  q goes to q_out, k and v (v
+ * unchanged) to the caches at slots[t]; a slot outside [0, num_pages *
+ * page_size) writes nothing there (q_out is written for every row).  Slots
+ * must differ from one another.
+ *   q [T][Hq][d], k, v [T][Hkv][d], q_out [T][Hq][d]: strides of the token and
+ *   the head in elements (they may be views of one projection's output).
+ *   q_out may be q itself (same address and strides), else buffers may not overlap.
+ *   q_weight, k_weight: [d] of dtype, or NULL for no norm.  eps >= 0.
+ *   inv_freq: [rot/2] fp64 device array (NULL if rot == 0); rot a multiple of
+ *   16, at most d.  Hq or Hkv may be 0. */
+think_status_t think_norm_rope_append(const void *q, const int64_t q_strides[2], const void *k,
+                                      const int64_t k_strides[2], const void *v, const int64_t v_strides[2], int64_t T,
+                                      int Hq, int Hkv, int d, think_dtype_t dtype, const void *q_weight,
+                                      const void *k_weight, float eps, const double *inv_freq, int rot, int neighbours,
+                                      const int32_t *positions, const int64_t *slots, void *q_out,
+                                      const int64_t q_out_strides[2], void *k_cache, const int64_t k_cache_strides[3],
+                                      void *v_cache, const int64_t v_cache_strides[3], int num_pages, int page_size,
+                                      void *stream);
+/* think_paged_attn: causal attention of the new tokens over the pages; two
+ * launches.  The i-th new token of request b, of n_b = q_start[b+1] -
+ * q_start[b], has position p = kv_lens[b] - n_b + i (kv_lens counts the new
+ * tokens, whose keys are in the pages already) and sees the keys j <= p, with
+ * window > 0 only those with j > p - window:
+ *     out = sum_j softmax_j(scale * q . K_j) V_j
+ * for each query head h, over KV head h / G; a row that sees no key (p < 0)
+ * gets zeros.  Arithmetic: fp32 sums and softmax; bf16 rounds the softmax
+ * weights to bf16 before the product with V, as it rounds the output.
+ *   q, out   [T][Hq][d] of dtype, strides of the token and the head.  Rows
+ *            outside every request's range are not written.
+ *   max_new  the largest number of new tokens of a request, or 0 if not
+ *            known: it only helps to choose the kernel.
+ *   Keys and values of positions < kv_lens[b] must be finite; what the pages
+ * hold behind them, and pages that no row sees (before the window, behind the
+ * last token), may be anything, their table entries too.  A needed page outside
+ * the pool counts as zero keys and values, with THINK_DEVICE_BAD_PAGE in the
+ * status word.
+ *   workspace: think_paged_attn_workspace_size() bytes (it depends on T * G
+ * only up to 128 rows, and on nothing else), 16-byte aligned, zeroed once
+ * before its first use (the status word; the rest is scratch).  Results do not
+ * depend on timing.  Any Hq that is a multiple of Hkv (G <= 4096). */
+size_t think_paged_attn_workspace_size(int64_t T, int Hq, int Hkv, int d, think_dtype_t dtype);
+think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const void *k_cache,
+                                const int64_t k_cache_strides[3], const void *v_cache, const int64_t v_cache_strides[3],
+                                int num_pages, int page_size, const int32_t *block_table, int64_t table_ld,
+                                int max_blocks, const int32_t *q_start, const int32_t *kv_lens, int B, int64_t T,
+                                int max_new, int Hq, int Hkv, int d, think_dtype_t dtype, float scale, int window,
+                                void *out, const int64_t out_strides[2], void *workspace, size_t workspace_bytes,
+                                void *stream);
+/* think_gather_pages: one launch.  out[b][h][n][:] = row of position n for n <
+ * kv_lens[b] (kv_lens held to [0, max_blocks * page_size]), zeros behind it and
+ * for pages outside the pool; out contiguous [B][Hkv][N][d], N <= 2^30.  Zero
+ * rows add nothing to think_prune's channel scores, but they are tokens like
+ * others to the decode: prune requests of one length together. */
+think_status_t think_gather_pages(const void *cache, const int64_t cache_strides[3], int num_pages, int page_size,
+                                  const int32_t *block_table, int64_t table_ld, int max_blocks, const int32_t *kv_lens,
+                                  int B, int Hkv, int64_t N, int d, think_dtype_t dtype, void *out, void *stream);
 
 /* Zero a score or decode workspace (stream-ordered memset); the library
  * forgets the counter place it remembered for this address. */

@@ -34,6 +34,8 @@ THINK_DEVICE_TIMEOUT_EMPTY = 0x2
 THINK_DEVICE_TIMEOUT_READY = 0x4
 THINK_DEVICE_TIMEOUT_BARRIER = 0x8
 THINK_DEVICE_OOB = 0x10
+THINK_DEVICE_NO_PAGES = 0x20
+THINK_DEVICE_BAD_PAGE = 0x40
 
 EXPORTED = (
     "think_status_string", "think_t_from_lambda", "think_pruned_ld",
@@ -46,6 +48,8 @@ EXPORTED = (
     "think_compact_keys_ragged", "think_prune_adaptive", "think_pruned_decode_attn_ragged",
     "think_token_mass_workspace_size",
     "think_token_mass", "think_select_tokens_workspace_size", "think_select_tokens", "think_gather_tokens",
+    "think_extend_pages_workspace_size", "think_extend_pages", "think_norm_rope_append",
+    "think_paged_attn_workspace_size", "think_paged_attn", "think_gather_pages",
 )
 
 
@@ -114,6 +118,20 @@ def _load() -> ctypes.CDLL:
     lib.think_pruned_decode_attn_noalloc.argtypes = [P, P, I64, P, I64P, P, I, I, I, I64, I, I, I, F,
                                                      P, P]
     lib.think_pruned_decode_attn_noalloc.restype = I
+    lib.think_extend_pages_workspace_size.argtypes = []
+    lib.think_extend_pages_workspace_size.restype = SZ
+    lib.think_extend_pages.argtypes = [P, P, I, I, P, I64, I, P, I, P, I64, P, P, P, P, P, P, SZ, P]
+    lib.think_extend_pages.restype = I
+    lib.think_norm_rope_append.argtypes = [P, I64P, P, I64P, P, I64P, I64, I, I, I, I, P, P, F, P, I, I, P, P, P, I64P, P,
+                                           I64P, P, I64P, I, I, P]
+    lib.think_norm_rope_append.restype = I
+    lib.think_paged_attn_workspace_size.argtypes = [I64, I, I, I, I]
+    lib.think_paged_attn_workspace_size.restype = SZ
+    lib.think_paged_attn.argtypes = [P, I64P, P, I64P, P, I64P, I, I, P, I64, I, P, P, I, I64, I, I, I, I, I, F, I, P,
+                                     I64P, P, SZ, P]
+    lib.think_paged_attn.restype = I
+    lib.think_gather_pages.argtypes = [P, I64P, I, I, P, I64, I, P, I, I, I64, I, I, P, P]
+    lib.think_gather_pages.restype = I
     lib.think_workspace_init.argtypes = [P, SZ, P]
     lib.think_workspace_init.restype = I
     lib.think_read_device_status.argtypes = [P, ctypes.POINTER(ctypes.c_uint32), P]
@@ -486,6 +504,165 @@ class EvictedCache:
 
     def decode(self, q, out, scale=None, stream=None):
         self.pruned.decode(q, self.v_kept, out, scale=scale, stream=stream)
+
+
+# ------------------------------------------------------------ paged cache --
+
+def _on(where: str, *tensors):
+    """The device of the tensors (None skipped), which must all lie on it."""
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda or (device is not None and t.device != device):
+            raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: every tensor must lie on one GPU")
+        device = t.device
+    return device
+
+
+def _call(where: str, device, stream, fn, *args) -> None:
+    """Call a C entry point with `device` current, on `stream` (default: the
+    device's current stream)."""
+    index = device.index
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
+    if rc != THINK_OK:
+        raise ThinkError(rc, where)
+
+
+def _i64x(*xs):
+    return (ctypes.c_int64 * len(xs))(*xs)
+
+
+def _rows(where: str, t: torch.Tensor):
+    """Token and head strides of a [T,H,d] tensor with contiguous channels."""
+    if t.dim() != 3 or t.stride(2) != 1:
+        raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: expected a [T,H,d] tensor with contiguous channels")
+    return _i64x(t.stride(0), t.stride(1))
+
+
+def _pool(where: str, t: torch.Tensor):
+    """Page, head and row strides of a [pages,Hkv,page_size,d] tensor."""
+    if t.dim() != 4 or t.stride(3) != 1:
+        raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: expected a [pages,Hkv,page_size,d] tensor with contiguous channels")
+    return _i64x(t.stride(0), t.stride(1), t.stride(2))
+
+
+def _ints(where: str, dtype: torch.dtype, n: int, *tensors) -> None:
+    for t in tensors:
+        if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+            raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: expected contiguous {dtype} tensors of {n} elements")
+
+
+def _table(where: str, t: torch.Tensor, B: int) -> int:
+    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != B or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: expected a [{B},max_blocks] int32 block table")
+    return t.stride(0) if B > 1 else max(t.stride(0), t.shape[1])
+
+
+def think_extend_pages_workspace_size() -> int:
+    return lib.think_extend_pages_workspace_size()
+
+
+def think_extend_pages(new_lens: torch.Tensor, kv_lens: torch.Tensor, block_table: torch.Tensor, free_pages: torch.Tensor,
+                       free_count: torch.Tensor, page_size: int, kv_lens_out: torch.Tensor,
+                       free_count_out: torch.Tensor, q_start: torch.Tensor, positions: torch.Tensor,
+                       slots: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """new_lens, kv_lens [B], block_table [B,max_blocks], the stack free_pages with its height free_count [1] (int32)
+    -> kv_lens_out [B], free_count_out [1], q_start [B+1], positions [T] (int32), slots [T] (int64), fresh table entries."""
+    where = "think_extend_pages"
+    B, T = new_lens.shape[0], positions.shape[0]
+    device = _on(where, new_lens, kv_lens, block_table, free_pages, free_count, kv_lens_out, free_count_out, q_start,
+                 positions, slots, workspace)
+    _ints(where, torch.int32, B, new_lens, kv_lens, kv_lens_out)
+    _ints(where, torch.int32, 1, free_count, free_count_out)
+    _ints(where, torch.int32, B + 1, q_start)
+    _ints(where, torch.int32, T, positions)
+    _ints(where, torch.int64, T, slots)
+    _ints(where, torch.int32, free_pages.numel(), free_pages)
+    ld = _table(where, block_table, B)
+    _call(where, device, stream, lib.think_extend_pages, new_lens.data_ptr(), kv_lens.data_ptr(), B, int(page_size),
+          block_table.data_ptr(), ld, block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
+          free_count.data_ptr(), T, kv_lens_out.data_ptr(), free_count_out.data_ptr(), q_start.data_ptr(),
+          positions.data_ptr(), slots.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def think_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: torch.Tensor | None,
+                           k_weight: torch.Tensor | None, eps: float, inv_freq: torch.Tensor | None, neighbours: bool,
+                           positions: torch.Tensor, slots: torch.Tensor, q_out: torch.Tensor, k_cache: torch.Tensor,
+                           v_cache: torch.Tensor, stream=None) -> None:
+    """q [T,Hq,d], k, v [T,Hkv,d] -> q_out [T,Hq,d] (normed, turned) and the rows `slots` [T] int64 of k_cache, v_cache
+    [pages,Hkv,page_size,d] (k normed and turned).  inv_freq [rot/2] fp64 (None: no rotation), positions [T] int32."""
+    where = "think_norm_rope_append"
+    T, Hq, d = q.shape
+    Hkv = k.shape[1]
+    device = _on(where, q, k, v, q_weight, k_weight, inv_freq, positions, slots, q_out, k_cache, v_cache)
+    _ints(where, torch.int32, T, positions)
+    _ints(where, torch.int64, T, slots)
+    if inv_freq is not None:
+        _ints(where, torch.float64, inv_freq.numel(), inv_freq)
+    for w in (q_weight, k_weight):
+        if w is not None:
+            _ints(where, q.dtype, d, w)
+    if any(t.dtype != q.dtype for t in (k, v, q_out, k_cache, v_cache)) or k.shape != (T, Hkv, d) or v.shape != k.shape \
+            or q_out.shape != q.shape or k_cache.shape[1] != Hkv or k_cache.shape[3] != d or v_cache.shape != k_cache.shape:
+        raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: shapes or dtypes do not match")
+    _call(where, device, stream, lib.think_norm_rope_append, q.data_ptr(), _rows(where, q), k.data_ptr(), _rows(where, k),
+          v.data_ptr(), _rows(where, v), T, Hq, Hkv, d, _dtype(q), None if q_weight is None else q_weight.data_ptr(),
+          None if k_weight is None else k_weight.data_ptr(), float(eps),
+          None if inv_freq is None else inv_freq.data_ptr(), 0 if inv_freq is None else 2 * inv_freq.shape[0],
+          int(bool(neighbours)), positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(), _rows(where, q_out),
+          k_cache.data_ptr(), _pool(where, k_cache), v_cache.data_ptr(), _pool(where, v_cache), k_cache.shape[0],
+          k_cache.shape[2])
+
+
+def think_paged_attn_workspace_size(T: int, Hq: int, Hkv: int, d: int = 128, dtype: torch.dtype = torch.bfloat16) -> int:
+    return lib.think_paged_attn_workspace_size(int(T), Hq, Hkv, d, THINK_BF16 if dtype == torch.bfloat16 else THINK_F32)
+
+
+def think_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                     q_start: torch.Tensor, kv_lens: torch.Tensor, out: torch.Tensor, workspace: torch.Tensor,
+                     window: int = 0, scale: float | None = None, max_new: int = 0, stream=None) -> None:
+    """q [T,Hq,d], caches [pages,Hkv,page_size,d], block_table [B,max_blocks], q_start [B+1], kv_lens [B] (int32, with the
+    new tokens) -> out [T,Hq,d] of q's dtype: causal attention of the new tokens, with window > 0 over the last
+    `window` keys.  max_new: the largest number of new tokens of a request (0: not known)."""
+    where = "think_paged_attn"
+    T, Hq, d = q.shape
+    pages, Hkv, page_size, dk = k_cache.shape
+    B = kv_lens.shape[0]
+    device = _on(where, q, k_cache, v_cache, block_table, q_start, kv_lens, out, workspace)
+    _ints(where, torch.int32, B, kv_lens)
+    _ints(where, torch.int32, B + 1, q_start)
+    if any(t.dtype != q.dtype for t in (k_cache, v_cache, out)) or v_cache.shape != k_cache.shape or dk != d \
+            or out.shape != q.shape:
+        raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: shapes or dtypes do not match")
+    ld = _table(where, block_table, B)
+    _call(where, device, stream, lib.think_paged_attn, q.data_ptr(), _rows(where, q), k_cache.data_ptr(),
+          _pool(where, k_cache), v_cache.data_ptr(), _pool(where, v_cache), pages, page_size, block_table.data_ptr(), ld,
+          block_table.shape[1], q_start.data_ptr(), kv_lens.data_ptr(), B, T, int(max_new), Hq, Hkv, d, _dtype(q),
+          float(1.0 / float(d) ** 0.5 if scale is None else scale), int(window), out.data_ptr(), _rows(where, out),
+          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+
+def think_gather_pages(cache: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor, out: torch.Tensor,
+                       stream=None) -> None:
+    """cache [pages,Hkv,page_size,d], block_table [B,max_blocks], kv_lens [B] (int32) -> out [B,Hkv,N,d] (contiguous),
+    zeros behind a request's length."""
+    where = "think_gather_pages"
+    pages, Hkv, page_size, d = cache.shape
+    B = kv_lens.shape[0]
+    device = _on(where, cache, block_table, kv_lens, out)
+    _ints(where, torch.int32, B, kv_lens)
+    if out.dtype != cache.dtype or not out.is_contiguous() or out.dim() != 4 or out.shape[:2] != (B, Hkv) or out.shape[3] != d:
+        raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: out must be a contiguous [B,Hkv,N,d] tensor of the cache's dtype")
+    ld = _table(where, block_table, B)
+    _call(where, device, stream, lib.think_gather_pages, cache.data_ptr(), _pool(where, cache), pages, page_size,
+          block_table.data_ptr(), ld, block_table.shape[1], kv_lens.data_ptr(), B, Hkv, out.shape[2], d, _dtype(cache),
+          out.data_ptr())
 
 
 def think_workspace_init(workspace: torch.Tensor, stream=None) -> None:

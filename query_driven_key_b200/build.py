@@ -20,6 +20,7 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC",
     "-Xptxas", "-warn-spills",
     "-shared",
+    "--threads", "0",  # the source files compile beside each other
 ]
 
 

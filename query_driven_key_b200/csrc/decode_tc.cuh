@@ -77,25 +77,6 @@ __host__ __device__ inline TcLayout tc_layout(int T, int sk, int sv)
     return L;
 }
 
-// Bounded mbarrier wait that honours (and raises) the block's abort flag.
-__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag,
-                                        unsigned *status, unsigned code)
-{
-    if (*abort_flag) return false;
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    for (uint32_t spin = 0; spin < kWaitLimitSpins; ++spin) {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if (global_ns() - t0 > kWaitLimitNs) break;
-    }
-    *abort_flag = 1u;
-    atomicOr(status, code);
-    return false;
-}
-
 // Byte offset of element (row, col) in a K-major interleaved operand whose
 // rows are N (or M) and whose columns are K: 8 x 8 core matrices of 128 B,
 // consecutive along K (128 B apart), row groups of 8 `sbo` bytes apart.

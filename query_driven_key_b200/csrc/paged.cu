@@ -1,0 +1,264 @@
+// paged.cu -- host side of the paged cache's entry points declared in
+// include/think.h: argument validation, launch planning, launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "host.cuh"
+#include "paged_plan.cuh"
+#include "paged_simt.cuh"
+#include "pages.cuh"
+#include "rope.cuh"
+#include "think.h"
+
+namespace think {
+namespace {
+
+constexpr size_t kPagedHeader = 256;     // status word + reserved, start of a workspace
+constexpr int kPageStep = 16;            // page sizes are multiples of 16 rows
+constexpr int64_t kExtendRowsPerBlock = 4096;
+
+inline bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+inline bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+// Strides of `n` leading dimensions: non-negative multiples of 16 bytes.
+inline bool strides16(const int64_t *s, int n, size_t es)
+{
+    for (int i = 0; i < n; ++i)
+        if (s[i] < 0 || s[i] % (int64_t)(16 / es) != 0) return false;
+    return true;
+}
+
+// A block table of B rows: its pages and the tokens that a row can hold.
+think_status_t check_table(const int32_t *table, int64_t table_ld, int max_blocks, int page_size, int num_pages)
+{
+    if (page_size < 1 || max_blocks < 1 || num_pages < 1 || table_ld < max_blocks) return THINK_ERR_INVALID_ARG;
+    if (page_size % kPageStep != 0) return THINK_ERR_UNSUPPORTED;
+    if ((int64_t)max_blocks * page_size > kMaxPosition) return THINK_ERR_UNSUPPORTED;
+    if (!table) return THINK_ERR_INVALID_ARG;
+    return aligned4(table) ? THINK_OK : THINK_ERR_ALIGNMENT;
+}
+
+struct PagedPlan {
+    int rows;      // query rows of an item
+    int parts;     // blocks
+    int rows_cap;  // rows of a partial
+    size_t smem;
+};
+
+// fp32: items of 64 query rows (two blocks an SM), or of 16 where no request
+// has more rows than that.
+PagedPlan plan_paged(int64_t T, int G, int max_new)
+{
+    PagedPlan p;
+    p.rows = (int64_t)max_new * G <= 16 ? 16 : 64;
+    p.parts = kTargetSMs * 2;
+    p.smem = p.rows == 16 ? paged_simt_smem<16>() : paged_simt_smem<64>();
+    p.rows_cap = (int)std::min<int64_t>(64, T * G);
+    return p;
+}
+
+size_t paged_ws_bytes(int64_t T, int G)
+{
+    const int64_t rows = std::min<int64_t>(128, T * G);
+    return kPagedHeader + sizeof(float) * (size_t)kTargetSMs * 2 * 4 * (size_t)rows * kPartLd;
+}
+
+template <typename T, int R>
+think_status_t launch_paged_simt(const PagedArgs &a, const PagedPlan &p, cudaStream_t st)
+{
+    const void *kern = reinterpret_cast<const void *>(&paged_simt_kernel<T, R>);
+    if (!ensure_smem(kern, p.smem)) return THINK_ERR_CUDA;
+    const think_status_t rc = launch_pdl(paged_simt_kernel<T, R>, dim3((unsigned)p.parts), dim3(kSimtThreads), p.smem, st, a);
+    if (rc != THINK_OK) return rc;
+    return launch_pdl(paged_merge_kernel<T, R, kSimtBN, false>, dim3((unsigned)(p.parts - 1), kMergeSlices),
+                      dim3(kMergeThreads), 0, st, a);
+}
+
+template <typename T>
+think_status_t launch_rope(bool neighbours, int64_t rows, const RopeArgs &a, cudaStream_t st)
+{
+    return neighbours ? launch_pdl(norm_rope_append_kernel<T, true>, dim3((unsigned)rows), dim3(kRopeThreads), 0, st, a)
+                      : launch_pdl(norm_rope_append_kernel<T, false>, dim3((unsigned)rows), dim3(kRopeThreads), 0, st, a);
+}
+
+}  // namespace
+}  // namespace think
+
+using namespace think;
+
+extern "C" {
+
+size_t think_extend_pages_workspace_size(void) { return kPagedHeader; }
+
+think_status_t think_extend_pages(const int32_t *new_lens, const int32_t *kv_lens, int B, int page_size, int32_t *block_table,
+                                  int64_t table_ld, int max_blocks, const int32_t *free_pages, int n_free,
+                                  const int32_t *free_count, int64_t T, int32_t *kv_lens_out, int32_t *free_count_out,
+                                  int32_t *q_start, int32_t *positions, int64_t *slots, void *workspace,
+                                  size_t workspace_bytes, void *stream)
+{
+    if (B < 0 || T < 0 || n_free < 0) return THINK_ERR_INVALID_ARG;
+    if (T > INT32_MAX) return THINK_ERR_UNSUPPORTED;
+    if (B == 0) return THINK_OK;
+    const think_status_t rc = check_table(block_table, table_ld, max_blocks, page_size, 1);
+    if (rc != THINK_OK) return rc;
+    if (!new_lens || !kv_lens || !free_count || !kv_lens_out || !free_count_out || !q_start || !workspace ||
+        (n_free > 0 && !free_pages) || (T > 0 && (!positions || !slots)))
+        return THINK_ERR_INVALID_ARG;
+    if (!aligned4(new_lens) || !aligned4(kv_lens) || !aligned4(free_pages) || !aligned4(free_count) ||
+        !aligned4(kv_lens_out) || !aligned4(free_count_out) || !aligned4(q_start) || !aligned4(positions) ||
+        !aligned8(slots) || !aligned16(workspace))
+        return THINK_ERR_ALIGNMENT;
+    if (workspace_bytes < think_extend_pages_workspace_size()) return THINK_ERR_WORKSPACE;
+    ExtendArgs a;
+    a.new_lens = new_lens;
+    a.kv_lens = kv_lens;
+    a.free_pages = free_pages;
+    a.free_count = free_count;
+    a.kv_lens_out = kv_lens_out;
+    a.free_count_out = free_count_out;
+    a.table = block_table;
+    a.q_start = q_start;
+    a.positions = positions;
+    a.slots = slots;
+    a.status = static_cast<unsigned *>(workspace);
+    a.table_ld = table_ld;
+    a.T = T;
+    a.limit = (int64_t)max_blocks * page_size;
+    a.B = B;
+    a.page_size = page_size;
+    a.n_free = n_free;
+    // one block for a decode step's few rows; up to a cluster of eight for prompts
+    int blocks = 1;
+    while (blocks < kPagesMaxCluster && T > blocks * kExtendRowsPerBlock) blocks *= 2;
+    return launch_pdl_cluster(extend_pages_kernel, dim3((unsigned)blocks), dim3(kPagesThreads), 0,
+                              static_cast<cudaStream_t>(stream), blocks, a);
+}
+
+think_status_t think_norm_rope_append(const void *q, const int64_t q_strides[2], const void *k, const int64_t k_strides[2],
+                                      const void *v, const int64_t v_strides[2], int64_t T, int Hq, int Hkv, int d,
+                                      think_dtype_t dtype, const void *q_weight, const void *k_weight, float eps,
+                                      const double *inv_freq, int rot, int neighbours, const int32_t *positions,
+                                      const int64_t *slots, void *q_out, const int64_t q_out_strides[2], void *k_cache,
+                                      const int64_t k_cache_strides[3], void *v_cache, const int64_t v_cache_strides[3],
+                                      int num_pages, int page_size, void *stream)
+{
+    if (T < 0 || Hq < 0 || Hkv < 0 || !dtype_ok(dtype)) return THINK_ERR_INVALID_ARG;
+    if (d != kD) return THINK_ERR_UNSUPPORTED;
+    if (T == 0 || Hq + Hkv == 0) return THINK_OK;
+    if (T > INT32_MAX || Hq > 65535 || Hkv > 65535) return THINK_ERR_UNSUPPORTED;
+    if (rot < 0 || rot > kD || page_size < 1 || num_pages < 1 || !(eps >= 0.f) || !std::isfinite(eps)) return THINK_ERR_INVALID_ARG;
+    if (rot % 16 != 0 || page_size % kPageStep != 0) return THINK_ERR_UNSUPPORTED;
+    if ((Hq > 0 && (!q || !q_strides || !q_out || !q_out_strides)) || (rot > 0 && !inv_freq) || !positions || !slots)
+        return THINK_ERR_INVALID_ARG;
+    if (Hkv > 0 && (!k || !k_strides || !v || !v_strides || !k_cache || !k_cache_strides || !v_cache || !v_cache_strides))
+        return THINK_ERR_INVALID_ARG;
+    const size_t es = esize(dtype);
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !aligned16(q_weight) || !aligned16(k_weight) || !aligned8(inv_freq) || !aligned4(positions) || !aligned8(slots))
+        return THINK_ERR_ALIGNMENT;
+    if ((Hq > 0 && (!strides16(q_strides, 2, es) || !strides16(q_out_strides, 2, es))) ||
+        (Hkv > 0 && (!strides16(k_strides, 2, es) || !strides16(v_strides, 2, es) || !strides16(k_cache_strides, 3, es) ||
+                     !strides16(v_cache_strides, 3, es))))
+        return THINK_ERR_ALIGNMENT;
+    RopeArgs a = {};
+    a.q = q, a.k = k, a.v = v, a.wq = q_weight, a.wk = k_weight;
+    a.q_out = q_out, a.k_cache = k_cache, a.v_cache = v_cache;
+    a.inv_freq = inv_freq;
+    a.positions = positions;
+    a.slots = slots;
+    if (Hq > 0) a.q_st = q_strides[0], a.q_sh = q_strides[1], a.qo_st = q_out_strides[0], a.qo_sh = q_out_strides[1];
+    if (Hkv > 0) {
+        a.k_st = k_strides[0], a.k_sh = k_strides[1], a.v_st = v_strides[0], a.v_sh = v_strides[1];
+        a.kc_sp = k_cache_strides[0], a.kc_sh = k_cache_strides[1], a.kc_sn = k_cache_strides[2];
+        a.vc_sp = v_cache_strides[0], a.vc_sh = v_cache_strides[1], a.vc_sn = v_cache_strides[2];
+    }
+    a.num_slots = (int64_t)num_pages * page_size;
+    a.Hq = Hq, a.Hkv = Hkv, a.rot = rot, a.page_size = page_size;
+    a.eps = eps;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return dtype == THINK_BF16 ? launch_rope<__nv_bfloat16>(neighbours != 0, T, a, st) : launch_rope<float>(neighbours != 0, T, a, st);
+}
+
+size_t think_paged_attn_workspace_size(int64_t T, int Hq, int Hkv, int d, think_dtype_t dtype)
+{
+    if (T < 0 || Hkv <= 0 || Hq < Hkv || Hq % Hkv != 0 || d != kD || !dtype_ok(dtype)) return 0;
+    return paged_ws_bytes(T, Hq / Hkv);
+}
+
+think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const void *k_cache,
+                                const int64_t k_cache_strides[3], const void *v_cache, const int64_t v_cache_strides[3],
+                                int num_pages, int page_size, const int32_t *block_table, int64_t table_ld, int max_blocks,
+                                const int32_t *q_start, const int32_t *kv_lens, int B, int64_t T, int max_new, int Hq,
+                                int Hkv, int d, think_dtype_t dtype, float scale, int window, void *out,
+                                const int64_t out_strides[2], void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (B < 0 || T < 0 || Hq < 0 || Hkv < 0 || window < 0 || max_new < 0 || !dtype_ok(dtype)) return THINK_ERR_INVALID_ARG;
+    if (d != kD) return THINK_ERR_UNSUPPORTED;
+    if (B == 0 || T == 0 || Hkv == 0) return THINK_OK;
+    if (Hq < Hkv || Hq % Hkv != 0 || !std::isfinite(scale)) return THINK_ERR_INVALID_ARG;
+    const int G = Hq / Hkv;
+    if (Hkv > 65535 || G > 4096 || T > INT32_MAX || T * G > INT32_MAX - 4096) return THINK_ERR_UNSUPPORTED;
+    const think_status_t rc = check_table(block_table, table_ld, max_blocks, page_size, num_pages);
+    if (rc != THINK_OK) return rc;
+    if (!q || !q_strides || !k_cache || !k_cache_strides || !v_cache || !v_cache_strides || !q_start || !kv_lens || !out ||
+        !out_strides || !workspace)
+        return THINK_ERR_INVALID_ARG;
+    const size_t es = esize(dtype);
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace) ||
+        !aligned4(q_start) || !aligned4(kv_lens) || !strides16(q_strides, 2, es) || !strides16(out_strides, 2, es) ||
+        !strides16(k_cache_strides, 3, es) || !strides16(v_cache_strides, 3, es))
+        return THINK_ERR_ALIGNMENT;
+    if (workspace_bytes < paged_ws_bytes(T, G)) return THINK_ERR_WORKSPACE;
+    const PagedPlan p = plan_paged(T, G, max_new > 0 ? (int)std::min<int64_t>(max_new, T) : (int)T);
+    PagedArgs a = {};
+    a.q = q, a.k = k_cache, a.v = v_cache, a.out = out;
+    a.q_start = q_start, a.kv_lens = kv_lens, a.table = block_table;
+    a.status = static_cast<unsigned *>(workspace);
+    a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + kPagedHeader);
+    a.q_st = q_strides[0], a.q_sh = q_strides[1], a.o_st = out_strides[0], a.o_sh = out_strides[1];
+    a.k_sp = k_cache_strides[0], a.k_sh = k_cache_strides[1], a.k_sn = k_cache_strides[2];
+    a.v_sp = v_cache_strides[0], a.v_sh = v_cache_strides[1], a.v_sn = v_cache_strides[2];
+    a.table_ld = table_ld;
+    a.B = B, a.T = (int)T, a.Hkv = Hkv, a.G = G;
+    a.page_size = page_size, a.num_pages = num_pages, a.limit = max_blocks * page_size, a.window = window;
+    a.rows_cap = p.rows_cap, a.parts = p.parts;
+    a.scale_log2 = scale * 1.44269504088896341f;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == THINK_BF16)
+        return p.rows == 16 ? launch_paged_simt<__nv_bfloat16, 16>(a, p, st) : launch_paged_simt<__nv_bfloat16, 64>(a, p, st);
+    return p.rows == 16 ? launch_paged_simt<float, 16>(a, p, st) : launch_paged_simt<float, 64>(a, p, st);
+}
+
+think_status_t think_gather_pages(const void *cache, const int64_t cache_strides[3], int num_pages, int page_size,
+                                  const int32_t *block_table, int64_t table_ld, int max_blocks, const int32_t *kv_lens,
+                                  int B, int Hkv, int64_t N, int d, think_dtype_t dtype, void *out, void *stream)
+{
+    if (B < 0 || Hkv < 0 || N < 0 || !dtype_ok(dtype)) return THINK_ERR_INVALID_ARG;
+    if (d != kD) return THINK_ERR_UNSUPPORTED;
+    if (B == 0 || Hkv == 0 || N == 0) return THINK_OK;
+    const int64_t heads = (int64_t)B * Hkv;
+    if (heads > 65535 || N > kMaxPosition) return THINK_ERR_UNSUPPORTED;
+    const think_status_t rc = check_table(block_table, table_ld, max_blocks, page_size, num_pages);
+    if (rc != THINK_OK) return rc;
+    if (!cache || !cache_strides || !kv_lens || !out) return THINK_ERR_INVALID_ARG;
+    const size_t es = esize(dtype);
+    if (!aligned16(cache) || !aligned16(out) || !aligned4(kv_lens) || !strides16(cache_strides, 3, es)) return THINK_ERR_ALIGNMENT;
+    const int rows = kGatherThreads / (kD / (int)(16 / es)) * kGatherRows;
+    const dim3 grid((unsigned)ceil_div(N, rows), (unsigned)heads);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dtype == THINK_BF16)
+        return launch_pdl(gather_pages_kernel<__nv_bfloat16>, grid, dim3(kGatherThreads), 0, st,
+                          static_cast<const __nv_bfloat16 *>(cache), cache_strides[0], cache_strides[1], cache_strides[2],
+                          num_pages, page_size, block_table, table_ld, max_blocks, kv_lens, Hkv, N,
+                          static_cast<__nv_bfloat16 *>(out));
+    return launch_pdl(gather_pages_kernel<float>, grid, dim3(kGatherThreads), 0, st, static_cast<const float *>(cache),
+                      cache_strides[0], cache_strides[1], cache_strides[2], num_pages, page_size, block_table, table_ld,
+                      max_blocks, kv_lens, Hkv, N, static_cast<float *>(out));
+}
+
+}  // extern "C"

@@ -1,0 +1,304 @@
+// paged_plan.cuh -- how the attention of new tokens over the paged cache is
+// divided among the thread blocks, and the merge of what the division cut.
+//
+// Query rows: row r of request b is its new token r / G and query head r % G of
+// the KV head's group, so that the G heads that share keys fill a tile
+// together.  An item is (request, KV head, tile of R rows); its work is the
+// number of BN-key tiles that any of its rows sees (at least 1, so that rows
+// that see nothing are still written).  The items' key tiles form one sequence,
+// requests first, then heads, then row tiles; block i of P takes the i-th of P
+// equal parts of it.  Whatever the mix of lengths, all blocks get the same work
+// to within one key tile; an item that a part's border cuts is computed in
+// pieces, each piece leaves its (max, sum, O) in the workspace, and
+// merge_kernel joins them in order.  Lengths stay on the device: the plan is
+// recomputed from q_start and kv_lens by every launch, so that a captured
+// launch follows the lengths of each replay.
+#pragma once
+
+#include "pages.cuh"
+#include "ptx.cuh"
+
+namespace think {
+
+struct PagedArgs {
+    const void *q, *k, *v;
+    void *out;
+    const int32_t *q_start, *kv_lens, *table;
+    unsigned *status;
+    float *part;  // [blocks][2 pieces][2 sides][rows_cap][kPartLd]
+    int64_t q_st, q_sh, o_st, o_sh;
+    int64_t k_sp, k_sh, k_sn, v_sp, v_sh, v_sn;
+    int64_t table_ld;
+    int B, T, Hkv, G, page_size, num_pages, limit, window;
+    int rows_cap;  // rows of a partial that may hold data
+    int parts;     // blocks of the attention launch
+    float scale_log2;
+};
+
+constexpr int kPartLd = kD + 2;  // O[128], max, sum of a row
+
+struct Request {
+    int row0, n, kv;  // first row of q, new tokens, tokens with the new ones
+};
+
+// Lengths and offsets from the device arrays, held to the buffers' bounds.
+__device__ __forceinline__ Request load_request(const PagedArgs &a, int b)
+{
+    Request s;
+    s.row0 = min(max(a.q_start[b], 0), a.T);
+    s.n = min(max(a.q_start[b + 1], s.row0), a.T) - s.row0;
+    s.kv = min(max(a.kv_lens[b], 0), a.limit);
+    return s;
+}
+
+// The keys that some row of row tile qt sees: [lo, hi), and the range of key
+// tiles [j0, j1) that holds them (one empty tile if there are none).
+struct TileRange {
+    int lo, hi, j0, j1;
+};
+template <int R, int BN>
+__device__ __forceinline__ TileRange tile_range(const PagedArgs &a, const Request &s, int qt)
+{
+    const int rows = s.n * a.G;
+    const int r0 = qt * R, r1 = min(r0 + R, rows) - 1;
+    const int p0 = s.kv - s.n + r0 / a.G, p1 = s.kv - s.n + r1 / a.G;  // first and last position
+    TileRange t;
+    t.lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
+    t.hi = max(p1 + 1, 0);
+    if (t.hi <= t.lo) {
+        t.lo = t.hi = t.j0 = 0;
+        t.j1 = 1;
+    } else {
+        t.j0 = t.lo / BN;
+        t.j1 = (t.hi + BN - 1) / BN;
+    }
+    return t;
+}
+
+template <int R>
+__device__ __forceinline__ int row_tiles(const PagedArgs &a, const Request &s)
+{
+    return (s.n * a.G + R - 1) / R;
+}
+
+// Key tiles of one KV head of request b.
+template <int R, int BN>
+__device__ __forceinline__ int64_t head_units(const PagedArgs &a, const Request &s)
+{
+    const int nt = row_tiles<R>(a, s);
+    int64_t u = 0;
+    for (int qt = 0; qt < nt; ++qt) {
+        const TileRange t = tile_range<R, BN>(a, s, qt);
+        u += t.j1 - t.j0;
+    }
+    return u;
+}
+
+// A place in the sequence of key tiles.
+struct Place {
+    int b, h, qt, off;  // the item, and the key tiles of it that lie before the place
+};
+
+// Scratch of plan(): one block's.
+struct PlanSmem {
+    int64_t ws[33];
+    Place place;
+};
+
+// The total number of key tiles and the place of tile *first (a function of
+// the total); all NT threads call it.  Thread t keeps request t's share where
+// B <= NT, so that the lengths are read once.
+template <int R, int BN, int NT, typename First>
+__device__ __forceinline__ int64_t plan(const PagedArgs &a, PlanSmem *sm, First first)
+{
+    static_assert(NT % 32 == 0 && NT <= 1024, "whole warps");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int64_t mine = 0, sum = 0;
+    for (int b = tid; b < a.B; b += NT) {
+        mine = head_units<R, BN>(a, load_request(a, b)) * a.Hkv;
+        sum += mine;
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) sm->ws[warp] = sum;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < NT / 32; ++w) total += sm->ws[w];
+    __syncthreads();
+    const int64_t u = first(total);
+    int64_t base = 0;
+    for (int b0 = 0; b0 < a.B && base <= u; b0 += NT) {
+        const int b = b0 + tid;
+        const int64_t x0 = a.B <= NT ? mine : (b < a.B ? head_units<R, BN>(a, load_request(a, b)) * a.Hkv : 0);
+        int64_t x = x0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += y;
+        }
+        if (lane == 31) sm->ws[warp] = x;
+        __syncthreads();
+        int64_t chunk = 0;
+        for (int w = 0; w < NT / 32; ++w) {
+            if (w == warp) x += chunk;
+            chunk += sm->ws[w];
+        }
+        x += base;
+        if (u >= x - x0 && u < x) {  // this thread's request holds the place
+            const Request s = load_request(a, b);
+            const int64_t uh = x0 / a.Hkv;
+            int64_t rem = u - (x - x0);
+            Place p;
+            p.b = b;
+            p.h = (int)(rem / uh);
+            rem -= p.h * uh;
+            for (p.qt = 0;; ++p.qt) {
+                const TileRange t = tile_range<R, BN>(a, s, p.qt);
+                if (rem < t.j1 - t.j0) break;
+                rem -= t.j1 - t.j0;
+            }
+            p.off = (int)rem;
+            sm->place = p;
+        }
+        base += chunk;
+        __syncthreads();
+    }
+    return total;
+}
+
+// First key tile of part `part` of the min(parts, total) parts, none of which
+// is empty; total for the parts behind the last one.
+__device__ __forceinline__ int64_t part_begin(int64_t total, int part, int parts)
+{
+    const int64_t n = min((int64_t)parts, total);
+    return part >= n ? total : total / n * part + total % n * part / n;
+}
+
+// Walk over the items of a part: the current item's piece [j0, j1) of key
+// tiles, and whether the piece is the whole item.
+template <int R, int BN>
+struct Walk {
+    const PagedArgs &a;
+    Place p;
+    Request s;
+    int64_t left;   // key tiles of the part from this item on
+    TileRange t;    // the item
+    int j0, j1;     // the piece
+    bool whole, head;  // head: the piece begins with the item
+    __device__ __forceinline__ Walk(const PagedArgs &args, const Place &place, int64_t units) : a(args), p(place), left(units)
+    {
+        if (left > 0) {
+            s = load_request(a, p.b);
+            set();
+        }
+    }
+    __device__ __forceinline__ void set()
+    {
+        t = tile_range<R, BN>(a, s, p.qt);
+        j0 = t.j0 + p.off;
+        j1 = (int)min((int64_t)t.j1, j0 + left);
+        head = p.off == 0;
+        whole = head && j1 == t.j1;
+    }
+    __device__ __forceinline__ bool live() const { return left > 0; }
+    __device__ __forceinline__ void next()
+    {
+        left -= j1 - j0;
+        if (left <= 0) return;
+        p.off = 0;
+        if (++p.qt == row_tiles<R>(a, s)) {
+            p.qt = 0;
+            if (++p.h == a.Hkv) {
+                p.h = 0;
+                do {  // the sequence has `left` more tiles: a request with rows follows
+                    if (++p.b == a.B) {
+                        left = 0;
+                        return;
+                    }
+                    s = load_request(a, p.b);
+                } while (s.n == 0);
+            }
+        }
+        set();
+    }
+};
+
+// Partial of piece `piece` (0: continues an item that an earlier part began,
+// 1: begins an item that a later part continues) and side (the two halves of a
+// block's work on the piece, where it has two).
+__device__ __forceinline__ float *part_at(const PagedArgs &a, int part, int piece, int side)
+{
+    return a.part + ((int64_t)((part * 2 + piece) * 2 + side)) * a.rows_cap * kPartLd;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_out4(T *p, float4 x);
+template <>
+__device__ __forceinline__ void store_out4<float>(float *p, float4 x)
+{
+    *reinterpret_cast<float4 *>(p) = x;
+}
+template <>
+__device__ __forceinline__ void store_out4<__nv_bfloat16>(__nv_bfloat16 *p, float4 x)
+{
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2 *>(p) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+}
+
+// Join the pieces of the item that the border between parts c - 1 and c cuts,
+// if that is the first border inside the item (blockIdx.x = c - 1; blockIdx.y
+// and the warps share the rows).  In order of the parts, so that the result
+// does not depend on timing:
+//     m = max m_i,  l = sum l_i 2^(m_i - m),  out = sum O_i 2^(m_i - m) / l.
+// A row that sees no key has l = 0 and gets zeros.
+constexpr int kMergeThreads = 256;
+constexpr int kMergeSlices = 8;
+
+template <typename T, int R, int BN, bool TWO_SIDES>
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedArgs a)
+{
+    __shared__ PlanSmem sm;
+    const int c = (int)blockIdx.x + 1;
+    const int64_t total = plan<R, BN, kMergeThreads>(a, &sm, [&](int64_t n) { return part_begin(n, c, a.parts); });
+    const int64_t u = part_begin(total, c, a.parts);
+    grid_dependency_wait();  // every block waits, so that this grid ends after the attention
+    if (u >= total) return;
+    const Place p = sm.place;
+    const int64_t start = u - p.off;  // the item's first key tile in the sequence
+    if (p.off == 0 || part_begin(total, c - 1, a.parts) > start) return;
+    const Request s = load_request(a, p.b);
+    const TileRange t = tile_range<R, BN>(a, s, p.qt);
+    const int64_t end = start + (t.j1 - t.j0);
+    int last = c;  // the last part that holds a piece of the item
+    while (part_begin(total, last + 1, a.parts) < end) ++last;
+    const int rows = min(R, s.n * a.G - p.qt * R);
+    const int lane = threadIdx.x & 31;
+    const bool two_sides = TWO_SIDES && rows <= R / 2;  // the two sides hold the same rows
+    for (int r = (int)blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); r < rows;
+         r += kMergeSlices * (kMergeThreads / 32)) {
+        const int side0 = TWO_SIDES && !two_sides ? r / (R / 2) : 0;
+        const int row = TWO_SIDES && !two_sides ? r % (R / 2) : r;
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = c - 1; i <= last; ++i)
+            for (int side = side0; side <= (two_sides ? 1 : side0); ++side) {
+                const float *x = part_at(a, i, i == c - 1 ? 1 : 0, side) + (int64_t)row * kPartLd;
+                const float mi = __ldcg(x + kD), li = __ldcg(x + kD + 1);
+                const float2 a0 = __ldcg(reinterpret_cast<const float2 *>(x) + 2 * lane);
+                const float2 a1 = __ldcg(reinterpret_cast<const float2 *>(x) + 2 * lane + 1);
+                const float mn = fmaxf(m, mi), ref = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2f(m - ref), g = exp2f(mi - ref);
+                o.x = o.x * f + a0.x * g, o.y = o.y * f + a0.y * g;
+                o.z = o.z * f + a1.x * g, o.w = o.w * f + a1.y * g;
+                l = l * f + li * g;
+                m = mn;
+            }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const int gr = p.qt * R + r, tok = gr / a.G, g = gr % a.G;
+        store_out4(static_cast<T *>(a.out) + (int64_t)(s.row0 + tok) * a.o_st + (int64_t)(p.h * a.G + g) * a.o_sh + 4 * lane,
+                   make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    }
+}
+
+}  // namespace think

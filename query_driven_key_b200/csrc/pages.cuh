@@ -1,0 +1,188 @@
+// pages.cuh -- the paged cache's bookkeeping and the way out of it: block
+// tables and slot maps from request lengths, and the gather of a request's
+// pages into the contiguous layout that the channel pruning reads.
+//
+// A pool of num_pages pages of page_size token rows holds the keys (another
+// the values) of every request; page block_table[b][j] of the pool holds the
+// positions [j * page_size, (j + 1) * page_size) of request b, and the slot of
+// a position is page * page_size + its row in the page.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace think {
+
+constexpr int kPagesThreads = 1024;
+constexpr int kPagesMaxCluster = 8;
+constexpr int kMaxPosition = 1 << 30;  // positions and lengths stay below, so that tile arithmetic fits 32 bits
+
+struct ExtendArgs {
+    const int32_t *new_lens, *free_pages, *free_count;
+    const int32_t *kv_lens;
+    int32_t *kv_lens_out, *free_count_out, *table, *q_start, *positions;
+    int64_t *slots;
+    unsigned *status;
+    int64_t table_ld, T, limit;  // limit: the tokens that a table row can hold
+    int B, page_size, n_free;
+};
+
+// Inclusive scan of one value a thread over the block (kPagesThreads
+// threads); *total receives the block's sum.  `ws` holds 33 words.
+__device__ __forceinline__ int64_t block_scan_i64(int64_t x, int64_t *ws, int64_t *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) ws[warp] = x;
+    __syncthreads();
+    if (warp == 0) {
+        int64_t s = ws[lane];
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, s, d);
+            if (lane >= d) s += y;
+        }
+        ws[lane] = s;
+    }
+    __syncthreads();
+    x += warp ? ws[warp - 1] : 0;
+    *total = ws[31];
+    __syncthreads();
+    return x;
+}
+
+// Every block of the (one) cluster scans the requests, 1024 at a time, and
+// keeps their row range, length and place in the free stack in shared memory;
+// then the cluster's threads share the new tokens: each finds its request by
+// binary search and writes its position and slot.  A page is fresh exactly
+// where its first row is a new token, so that token's thread writes the table
+// entry, and no thread reads an entry that another one writes.  kv_lens and
+// free_count may be the outputs themselves: every block has read a chunk's
+// lengths before block 0 writes them (cluster barrier).  Bound by latency: a
+// few dependent loads, a scan of ten shuffles and the slot stores.
+__global__ void __launch_bounds__(kPagesThreads) extend_pages_kernel(const ExtendArgs a)
+{
+    __shared__ int64_t ws[33];
+    __shared__ int64_t s_row[kPagesThreads + 1];   // first row of the request
+    __shared__ int s_len[kPagesThreads];           // tokens before
+    __shared__ int64_t s_free[kPagesThreads];      // pages handed out before it; -1: not admitted
+    const int tid = threadIdx.x;
+    const int rank = (int)blockIdx.x, blocks = (int)gridDim.x;
+    grid_dependency_wait();
+    const int64_t count = min(max(*a.free_count, 0), a.n_free);
+    int64_t rows = 0, pages = 0, used = 0;  // over the chunks so far; used: pages of the admitted requests
+    unsigned bits = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kPagesThreads) {
+        const int b = b0 + tid;
+        const bool real = b < a.B;
+        const int n = real ? min(max(a.new_lens[b], 0), kMaxPosition) : 0;
+        const int len = real ? min(max(a.kv_lens[b], 0), kMaxPosition) : 0;
+        int64_t total, taken;
+        const int64_t row_end = rows + block_scan_i64(n, ws, &total);
+        // a request whose tokens do not fit its table row or the row arrays takes no page
+        const bool fits = (int64_t)len + n <= a.limit && row_end <= a.T;
+        const int need = fits ? (int)(((int64_t)len + n + a.page_size - 1) / a.page_size - ((int64_t)len + a.page_size - 1) / a.page_size) : 0;
+        const int64_t page_end = pages + block_scan_i64(need, ws, &taken);
+        const bool admitted = fits && (need == 0 || page_end <= count);
+        s_row[tid] = row_end - n;
+        s_len[tid] = len;
+        s_free[tid] = admitted ? page_end - need : -1;
+        if (tid == kPagesThreads - 1) s_row[kPagesThreads] = row_end;
+        if (real && !admitted && n > 0) bits |= THINK_DEVICE_NO_PAGES;
+        // pages of the admitted requests: the needy ones among them are a prefix
+        int64_t dummy;
+        block_scan_i64(admitted ? need : 0, ws, &dummy);
+        used += dummy;
+        cluster_sync_all();  // (and a block barrier) every block has read this chunk's lengths
+        if (rank == 0 && real) {
+            a.kv_lens_out[b] = admitted ? len + n : len;
+            a.q_start[b] = (int32_t)min(row_end - n, a.T);
+            if (b == a.B - 1) a.q_start[a.B] = (int32_t)min(row_end, a.T);
+        }
+        const int64_t lo = min(s_row[0], a.T), hi = min(s_row[kPagesThreads], a.T);
+        for (int64_t r = lo + (int64_t)rank * kPagesThreads + tid; r < hi; r += (int64_t)blocks * kPagesThreads) {
+            // the last request whose first row is <= r: it holds r (empty requests before it start there too)
+            int l = 0, h = kPagesThreads - 1;
+            while (l < h) {
+                const int m = (l + h + 1) >> 1;
+                if (s_row[m] <= r) l = m;
+                else h = m - 1;
+            }
+            const int len0 = s_len[l];
+            const int pos = len0 + (int)(r - s_row[l]);
+            int64_t slot = -1;
+            if (s_free[l] >= 0) {
+                const int j = pos / a.page_size, before = (len0 + a.page_size - 1) / a.page_size;
+                int64_t at = (int64_t)(b0 + l) * a.table_ld + j;
+                int page;
+                if (j < before) {
+                    page = a.table[at];
+                } else {
+                    page = a.free_pages[count - 1 - (s_free[l] + (j - before))];
+                    if (pos - j * a.page_size == 0) a.table[at] = page;
+                }
+                if (page >= 0) slot = (int64_t)page * a.page_size + (pos - j * a.page_size);
+                else bits |= THINK_DEVICE_BAD_PAGE;
+            }
+            a.positions[r] = pos;
+            a.slots[r] = slot;
+        }
+        rows += total;
+        pages += taken;
+        __syncthreads();  // the shared arrays are rewritten
+    }
+    // rows behind the last request
+    for (int64_t r = min(rows, a.T) + (int64_t)rank * kPagesThreads + tid; r < a.T; r += (int64_t)blocks * kPagesThreads) {
+        a.positions[r] = 0;
+        a.slots[r] = -1;
+    }
+    cluster_sync_all();  // every block has read free_count
+    if (rank == 0 && tid == 0) *a.free_count_out = (int32_t)(count - used);
+    if (bits) atomicOr(a.status, bits);
+}
+
+// Pages -> contiguous rows: out[b][h][n][:] = cache[table[b][n / page_size]][h][n % page_size][:]
+// for n < kv_lens[b], zero behind it (zero keys add nothing to a channel's
+// energy) and for pages outside the pool.  A copy, bound by HBM: one 16-byte
+// vector a lane, kGatherRows rows a thread, all loaded before the first store.
+constexpr int kGatherThreads = 256;
+constexpr int kGatherRows = 4;
+
+template <typename TIn>
+__global__ void __launch_bounds__(kGatherThreads)
+    gather_pages_kernel(const TIn *__restrict__ cache, int64_t sp, int64_t sh, int64_t sn, int num_pages, int page_size,
+                        const int32_t *__restrict__ table, int64_t table_ld, int max_blocks,
+                        const int32_t *__restrict__ kv_lens, int Hkv, int64_t N, TIn *__restrict__ out)
+{
+    constexpr int VEC = 16 / sizeof(TIn);
+    constexpr int LANES = kD / VEC;
+    constexpr int STEP = kGatherThreads / LANES;  // rows of one vector step
+    grid_dependency_wait();
+    const int head = blockIdx.y, b = head / Hkv, h = head % Hkv;
+    const int c = (threadIdx.x % LANES) * VEC;
+    const int64_t len = min((int64_t)max(kv_lens[b], 0), (int64_t)max_blocks * page_size);
+    const int64_t n0 = (int64_t)blockIdx.x * (STEP * kGatherRows) + threadIdx.x / LANES;
+    uint4 v[kGatherRows];
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i) {
+        const int64_t n = n0 + i * STEP;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (n < len && n < N) {
+            const int j = (int)n / page_size;
+            const int page = table[(int64_t)b * table_ld + j];
+            if ((unsigned)page < (unsigned)num_pages)
+                v[i] = *reinterpret_cast<const uint4 *>(cache + (int64_t)page * sp + (int64_t)h * sh +
+                                                        (int64_t)((int)n - j * page_size) * sn + c);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i) {
+        const int64_t n = n0 + i * STEP;
+        if (n < N) *reinterpret_cast<uint4 *>(out + ((int64_t)head * N + n) * kD + c) = v[i];
+    }
+}
+
+}  // namespace think

@@ -1,6 +1,7 @@
 // tc05.cuh -- inline-PTX helpers for the 5th-generation tensor cores (tcgen05)
 // and tensor memory (TMEM) on sm_100a: allocation, UMMA shared-memory and
-// instruction descriptors, MMA issue, commit to an mbarrier, TMEM loads.
+// instruction descriptors, MMA issue, commit to an mbarrier, TMEM loads, the
+// bounded wait of a block with an abort flag.
 #pragma once
 
 #include "ptx.cuh"
@@ -128,4 +129,24 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&r)[16])
 }
 
 }  // namespace tc05
+
+// Bounded mbarrier wait that honours (and raises) the block's abort flag.
+__device__ __forceinline__ bool tc_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag,
+                                        unsigned *status, unsigned code)
+{
+    if (*abort_flag) return false;
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t spin = 0; spin < kWaitLimitSpins; ++spin) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (global_ns() - t0 > kWaitLimitNs) break;
+    }
+    *abort_flag = 1u;
+    atomicOr(status, code);
+    return false;
+}
+
 }  // namespace think

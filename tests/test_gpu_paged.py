@@ -1,0 +1,381 @@
+"""The paged cache's kernels against plain fp64 and plain integers, on the GPU."""
+import math
+import random
+
+import pytest
+import torch
+
+import paged_plain as P
+
+pytestmark = pytest.mark.gpu
+qdk = pytest.importorskip("query_driven_key_b200")
+
+BF, F32 = torch.bfloat16, torch.float32
+SCALE = 1.0 / math.sqrt(128.0)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def ws(n):
+    return torch.zeros(n, dtype=torch.uint8, device="cuda")
+
+
+def attn_ws(T, Hq, Hkv, dtype):
+    """A workspace whose scratch holds NaN: only the status word has to be zero."""
+    w = torch.full((qdk.think_paged_attn_workspace_size(T, Hq, Hkv, dtype=dtype),), 255, dtype=torch.uint8, device="cuda")
+    w[:256] = 0
+    return w
+
+
+# ------------------------------------------------------------- page tables --
+
+def run_extend(new, ctx, table, free, count, page, T, in_place=False, n_free=None):
+    B = len(new)
+    lens, cnt = i32(ctx), i32([count])
+    o = dict(new=i32(new), lens=lens, table=i32(table).reshape(B, -1), free=i32(free), cnt=cnt,
+             lens_out=lens if in_place else i32([-5] * B), cnt_out=cnt if in_place else i32([-5]),
+             q_start=i32([-5] * (B + 1)), pos=torch.full((T,), -5, dtype=torch.int32, device="cuda"),
+             slots=torch.full((T,), -5, dtype=torch.int64, device="cuda"), ws=ws(qdk.think_extend_pages_workspace_size()))
+    qdk.think_extend_pages(o["new"], o["lens"], o["table"], o["free"], o["cnt"], page, o["lens_out"], o["cnt_out"],
+                           o["q_start"], o["pos"], o["slots"], o["ws"])
+    return o
+
+
+def check_extend(new, ctx, table, free, count, page, T, in_place=False):
+    o = run_extend(new, ctx, table, free, count, page, T, in_place)
+    lens, tab, left, q_start, pos, slots, refused = P.extend(new, ctx, table, free, count, page, T)
+    assert o["lens_out"].tolist() == lens
+    assert o["table"].tolist() == tab
+    assert o["cnt_out"].item() == left
+    assert o["q_start"].tolist() == q_start
+    assert o["pos"].tolist() == pos
+    assert o["slots"].tolist() == slots
+    status = qdk.think_read_device_status(o["ws"])
+    assert bool(status & qdk.THINK_DEVICE_NO_PAGES) == refused
+    return status
+
+
+def extend_case(B, hi_new, hi_ctx, page, seed, spare=5, width_extra=2):
+    r = random.Random(seed)
+    new = [r.randint(0, hi_new) for _ in range(B)]
+    ctx = [r.randint(0, hi_ctx) for _ in range(B)]
+    need = [P.pages_of(c, page) for c in ctx]
+    fresh = sum(P.pages_of(c + n, page) for n, c in zip(new, ctx)) - sum(need)
+    ids = list(range(sum(need) + fresh + spare))
+    r.shuffle(ids)
+    width = max(P.pages_of(c + n, page) for n, c in zip(new, ctx)) + width_extra
+    table = [[ids.pop() for _ in range(k)] + [-1] * (width - k) for k in need]
+    return new, ctx, table, ids, len(ids), page, sum(new)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,hi_new,hi_ctx,page", [
+    (1, 1, 0, 16), (1, 0, 40, 16), (3, 70, 100, 48), (32, 1, 500, 16), (1024, 1, 90, 16), (1025, 3, 60, 16),
+    (2100, 2, 40, 32), (7, 3000, 200, 64), (33, 1500, 4000, 256)])
+def test_extend(B, hi_new, hi_ctx, page, in_place):
+    status = check_extend(*extend_case(B, hi_new, hi_ctx, page, 11 * B + page), in_place=in_place)
+    assert status == 0
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_extend_runs_out(seed):
+    """Fewer free pages than wanted: the first requests are served, those that want none too."""
+    new, ctx, table, free, count, page, T = extend_case(40, 90, 200, 32, 900 + seed, spare=0)
+    for b in range(0, 40, 5):
+        new[b], T = 0, T - new[b]
+    for c in (0, 1, count // 3, count - 1):
+        check_extend(new, ctx, table, free, c, page, T, in_place=bool(seed & 1))
+
+
+def test_extend_no_room_in_table_or_rows():
+    # request 1 outgrows its table row (4 pages of 16), request 3 the 50 rows
+    check_extend([5, 30, 10, 20], [0, 40, 60, 0], [[-1] * 4, [1, 2, 3, -1], [4, 5, 6, 7], [-1] * 4], [8, 9, 10, 11], 4, 16, 50)
+    # more rows than tokens: position 0 and slot -1 behind the last request; less than nothing counts as none
+    check_extend([5, -3, 2], [0, 4, 17], [[-1] * 3, [0, -1, -1], [1, 2, -1]], [3, 4], 2, 16, 23)
+
+
+def test_extend_bad_pages():
+    status = check_extend([2, 20], [3, 5], [[-2, -1, -1], [4, -1, -1]], [7, -9, 5], 2, 16, 22)
+    assert status == qdk.THINK_DEVICE_BAD_PAGE
+
+
+def test_extend_count_above_stack_is_held_to_it():
+    o = run_extend([16], [0], [[-1, -1]], [3, 6], 1000, 16, 16)
+    assert o["table"].tolist() == [[6, -1]] and o["cnt_out"].item() == 1
+
+
+# ----------------------------------------------------- norm, rotation, pages --
+
+def rope_case(T, Hq, Hkv, dtype, rot, neighbours, norm, page, layout, seed, far=131072):
+    g = torch.Generator().manual_seed(seed)
+    heads = Hq + 2 * Hkv
+    qkv = torch.randn((T, heads, 128), generator=g).to(dtype).cuda()
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    wq, wk = ((1 + 0.3 * torch.randn((2, 128), generator=g)).to(dtype).cuda() if norm else (None, None))
+    freq = None if rot == 0 else (10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)).cuda()
+    pages = P.pages_of(T, page) + 2
+    slots = torch.randperm(pages * page, generator=g)[:T]
+    positions = torch.randint(0, far, (T,), generator=g).to(torch.int32)
+    shape = (pages, Hkv, page, 128) if layout == "hnd" else (pages, page, Hkv, 128)
+    caches = [torch.full(shape, 7.0, dtype=dtype, device="cuda") for _ in range(2)]
+    if layout == "nhd":
+        caches = [c.transpose(1, 2) for c in caches]
+    return q, k, v, wq, wk, freq, positions, slots, caches
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,dtype,rot,neighbours,norm,page,layout", [
+    (1, 32, 8, BF, 128, False, True, 16, "hnd"), (1, 1, 1, F32, 128, True, True, 16, "hnd"),
+    (37, 6, 2, BF, 96, False, True, 48, "nhd"), (37, 6, 2, BF, 96, True, False, 48, "nhd"),
+    (130, 40, 40, BF, 64, False, False, 64, "hnd"), (19, 3, 1, F32, 16, False, True, 32, "nhd"),
+    (64, 71, 3, F32, 128, False, True, 16, "hnd"), (5, 4, 2, BF, 0, False, True, 16, "hnd"),
+    (9, 4, 2, F32, 0, True, False, 16, "hnd"), (11, 16, 1, BF, 32, True, True, 128, "hnd")])
+def test_norm_rope_append(T, Hq, Hkv, dtype, rot, neighbours, norm, page, layout):
+    eps = 1e-6
+    q, k, v, wq, wk, freq, positions, slots, (kc, vc) = rope_case(T, Hq, Hkv, dtype, rot, neighbours, norm, page, layout, T + rot)
+    bad = {3, 8} if T > 8 else set()
+    for t, s in zip(sorted(bad), (-1, kc.shape[0] * page)):
+        slots[t] = s
+    q_out = torch.full((T, Hq, 128), 9.0, dtype=dtype, device="cuda")
+    qdk.think_norm_rope_append(q, k, v, wq, wk, eps, freq, neighbours, positions.cuda(), slots.cuda(), q_out, kc, vc)
+    cpu = lambda x: None if x is None else x.cpu()
+    want_k = torch.full((kc.shape[0] * page, Hkv, 128), 7.0, dtype=P.F64)
+    want_v, size_k = want_k.clone(), torch.zeros_like(want_k)
+    yk, sk = P.turned(cpu(k), cpu(wk), eps, cpu(freq), neighbours, positions)
+    for t in range(T):
+        if t not in bad:
+            want_k[slots[t]], size_k[slots[t]], want_v[slots[t]] = yk[t], sk[t], v[t].cpu().to(P.F64)
+    flat = lambda c: c.cpu().transpose(1, 2).reshape(-1, Hkv, 128).to(P.F64)
+    assert torch.equal(flat(vc), want_v)
+    # fp32 steps (u = 2^-24): the mean square of 128 terms 128 u, its root half of that, rsqrt, two products 6 u;
+    # cosine and sine to 8 u (argument and function); two products and a sum 3 u: below 90 u of |x1| + |x2|.
+    # One rounding to the type.
+    bound = lambda y, size: 90 * 2.0 ** -24 * size + P.HALF_STEP[dtype] * (1 + 2.0 ** -6) * y.abs() + 1e-30
+    assert ((flat(kc) - want_k).abs() <= bound(want_k, size_k)).all()
+    yq, sq = P.turned(cpu(q), cpu(wq), eps, cpu(freq), neighbours, positions)
+    assert ((q_out.cpu().to(P.F64) - yq).abs() <= bound(yq, sq)).all()
+
+
+def test_norm_rope_append_in_place_and_keys_only():
+    q, k, v, wq, wk, freq, positions, slots, (kc, vc) = rope_case(50, 8, 2, BF, 128, False, True, 16, "hnd", 5)
+    pos, sl = positions.cuda(), slots.cuda()
+    out = torch.empty((50, 8, 128), dtype=BF, device="cuda")
+    qdk.think_norm_rope_append(q, k, v, wq, wk, 1e-5, freq, False, pos, sl, out, kc, vc)
+    kc2, vc2 = torch.full_like(kc, 7.0), torch.full_like(vc, 7.0)
+    qdk.think_norm_rope_append(q[:, :0], k, v, None, wk, 1e-5, freq, False, pos, sl, out[:, :0], kc2, vc2)
+    assert torch.equal(kc, kc2) and torch.equal(vc, vc2)
+    qdk.think_norm_rope_append(q, k, v, wq, wk, 1e-5, freq, False, pos, sl, q, kc2, vc2)
+    assert torch.equal(q, out)
+
+
+def test_norm_of_zero_row_is_zero():
+    z = torch.zeros((1, 1, 128), dtype=BF, device="cuda")
+    kc, vc, out = (torch.ones((1, 1, 16, 128), dtype=BF, device="cuda") for _ in range(3))
+    w = torch.ones(128, dtype=BF, device="cuda")
+    out = torch.ones((1, 1, 128), dtype=BF, device="cuda")
+    qdk.think_norm_rope_append(z, z, z, w, w, 1e-6, None, False, i32([4]), torch.tensor([3], device="cuda"), out, kc, vc)
+    assert not out.any() and not kc[0, 0, 3].any() and kc.sum().item() == 15 * 128
+
+
+# ------------------------------------------------------------------ attention --
+
+def run_attn(x: P.Batch, Hq, Hkv, max_new=0, out=None, workspace=None, scale=SCALE):
+    w = attn_ws(x.T, Hq, Hkv, x.dtype) if workspace is None else workspace
+    out = torch.full((x.T, Hq, 128), 9.0, dtype=x.dtype, device="cuda") if out is None else out
+    qdk.think_paged_attn(x.q.cuda(), x.cache(x.k), x.cache(x.v), i32(x.table), i32(x.q_start), i32(x.lens), out, w,
+                         window=x.window, scale=scale, max_new=max_new)
+    assert qdk.think_read_device_status(w) == 0
+    return out
+
+
+def check_attn(x: P.Batch, Hq, Hkv, max_new=0, scale=SCALE):
+    got = run_attn(x, Hq, Hkv, max_new, scale=scale).cpu().to(P.F64)
+    want, size, logit = P.attend(x.q, x.k, x.v, x.table, x.q_start, x.lens, x.window, scale)
+    inside = x.q_start[-1]
+    assert (got[inside:] == 9.0).all(), "rows behind the last request were written"
+    got, want, size, logit = got[:inside], want[:inside], size[:inside], logit[:inside]
+    assert torch.isfinite(got).all()
+    bound = P.attend_bound(want, size, logit, x.dtype, max(x.lens + [1]))
+    over = (got - want).abs() / bound
+    assert over.max().item() <= 1.0, f"error {over.max().item():.3g} of the bound at {over.argmax().item()}"
+
+
+SHAPES = [
+    # new, ctx, Hq, Hkv, page, window
+    ([1], [0], 1, 1, 16, 0), ([1], [1], 4, 1, 16, 0), ([1], [700], 32, 8, 64, 0), ([1], [5000], 4, 1, 16, 0),
+    ([1, 1, 1, 1, 1], [0, 127, 128, 129, 1000], 8, 2, 16, 0), ([3], [0], 4, 4, 32, 0), ([17], [3], 2, 1, 48, 0),
+    ([128], [0], 4, 4, 64, 0), ([129], [0], 1, 1, 128, 0), ([300], [0], 4, 1, 16, 0), ([257], [300], 6, 2, 80, 0),
+    ([64, 0, 1, 33, 0, 2], [10, 50, 400, 0, 0, 127], 8, 2, 32, 0), ([5, 70], [30, 0], 7, 1, 16, 0),
+    ([40], [90], 12, 1, 256, 0), ([20, 1], [600, 900], 16, 2, 48, 0),
+    ([1, 200, 1], [900, 100, 30], 8, 2, 16, 64), ([300], [0], 4, 2, 32, 100), ([2, 40], [400, 300], 4, 1, 64, 1),
+    ([1, 1], [3000, 10], 8, 1, 16, 500), ([150], [500], 3, 1, 48, 333), ([600], [200], 2, 2, 112, 0)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("i", range(len(SHAPES)))
+def test_attn(i, dtype):
+    new, ctx, Hq, Hkv, page, window = SHAPES[i]
+    x = P.Batch(new, ctx, Hq, Hkv, page, dtype, 100 + i, window=window, layout="nhd" if i % 2 else "hnd", pad_rows=i % 3)
+    check_attn(x, Hq, Hkv, max_new=max(new) if i % 4 else 0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attn_rows_that_see_nothing(dtype):
+    """Fewer tokens cached than new ones: the first rows have positions below 0 and get zeros."""
+    x = P.Batch([6, 300, 4], [0, 0, 0], 4, 2, 16, dtype, 3, lens=[2, 170, 0])
+    check_attn(x, 4, 2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attn_large_logits(dtype):
+    """Sharp softmax: maxima that grow along the keys, and weights that underflow."""
+    x = P.Batch([40, 1], [700, 900], 8, 2, 32, dtype, 4, key_scale=12.0)
+    ramp = torch.linspace(0.02, 1.0, x.k.shape[0])[:, None, None, None]
+    x.k = (x.k.float() * ramp).to(dtype)
+    check_attn(x, 8, 2)
+    check_attn(x, 8, 2, scale=-0.05)
+    check_attn(x, 8, 2, scale=0.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attn_strides_and_views(dtype):
+    """q a view of a fused projection, out a view of a wider buffer, the table a view: canaries around stay."""
+    Hq, Hkv = 6, 2
+    x = P.Batch([33, 2], [100, 60], Hq, Hkv, 32, dtype, 8)
+    wide = torch.full((x.T, Hq + 3, 192), 5.0, dtype=dtype, device="cuda")
+    q = wide[:, 1:1 + Hq, 32:160]
+    q.copy_(x.q)
+    dst = torch.full((x.T + 2, Hq + 2, 256), 5.0, dtype=dtype, device="cuda")
+    out = dst[1:1 + x.T, 1:1 + Hq, 64:192]
+    tab = torch.full((3, len(x.table[0]) + 4), -1, dtype=torch.int32, device="cuda")
+    tab[:2, 2:-2] = i32(x.table)
+    w = attn_ws(x.T, Hq, Hkv, dtype)
+    qdk.think_paged_attn(q, x.cache(x.k), x.cache(x.v), tab[:2, 2:-2], i32(x.q_start), i32(x.lens), out, w)
+    assert torch.equal(out, run_attn(x, Hq, Hkv))
+    out.fill_(5.0)
+    assert (dst == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attn_bad_pages_count_as_zeros(dtype):
+    x = P.Batch([5, 40], [200, 90], 4, 2, 32, dtype, 9, poison=False)
+    x.table[0][2], x.table[1][1] = -1, x.k.shape[0]
+    w = attn_ws(x.T, 4, 2, dtype)
+    out = torch.empty((x.T, 4, 128), dtype=dtype, device="cuda")
+    qdk.think_paged_attn(x.q.cuda(), x.cache(x.k), x.cache(x.v), i32(x.table), i32(x.q_start), i32(x.lens), out, w)
+    assert qdk.think_read_device_status(w) == qdk.THINK_DEVICE_BAD_PAGE
+    pool = x.k.shape[0]
+    zero = torch.zeros_like(x.k[:1])
+    x.k, x.v = torch.cat([x.k, zero]), torch.cat([x.v, zero])
+    x.table[0][2] = x.table[1][1] = pool
+    assert torch.equal(out, run_attn(x, 4, 2))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attn_lengths_out_of_bounds_are_held(dtype):
+    """Garbage in the device arrays stays inside the buffers."""
+    x = P.Batch([8, 30], [100, 10], 4, 2, 16, dtype, 10, poison=False)
+    w = attn_ws(x.T, 4, 2, dtype)
+    canary = torch.full((x.T + 8, 4, 128), 5.0, dtype=dtype, device="cuda")
+    out = canary[4:4 + x.T]
+    for q_start, lens in (([0, 8, 10 ** 9], [10 ** 9, -4]), ([-50, 8, 3], [100, 2 ** 31 - 1]), ([40, 2, -1], [7, 40])):
+        qdk.think_paged_attn(x.q.cuda(), x.cache(x.k), x.cache(x.v), i32(x.table), i32(q_start), i32(lens), out, w)
+    torch.cuda.synchronize()
+    assert (canary[:4] == 5.0).all() and (canary[4 + x.T:] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attn_repeats_bit_for_bit_and_shares_a_workspace(dtype):
+    a = P.Batch([1, 90, 300], [2000, 10, 700], 8, 2, 32, dtype, 12)
+    b = P.Batch([2], [4000], 4, 1, 16, dtype, 13)
+    w = attn_ws(4096, 8, 1, dtype)
+    outs = [(run_attn(a, 8, 2, workspace=w), run_attn(b, 4, 1, workspace=w)) for _ in range(3)]
+    for p, q in outs[1:]:
+        assert torch.equal(p, outs[0][0]) and torch.equal(q, outs[0][1])
+
+
+def test_attn_many_requests():
+    """More requests than a block has threads, some empty, and long tables."""
+    r = random.Random(6)
+    new = [r.choice([0, 1, 1, 2]) for _ in range(700)]
+    ctx = [r.randint(0, 60) for _ in range(700)]
+    x = P.Batch(new, ctx, 2, 1, 16, BF, 14)
+    check_attn(x, 2, 1, max_new=2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_attn_captured_follows_the_lengths(dtype):
+    """One captured call, replayed after the lengths, rows and tables on the device changed."""
+    Hq, Hkv = 8, 2
+    xs = [P.Batch(n, c, Hq, Hkv, 16, dtype, 20 + i, pad_rows=80 - sum(n)) for i, (n, c) in enumerate(
+        [([1, 1, 40], [300, 20, 7]), ([30, 1, 2], [0, 900, 640]), ([80, 0, 0], [0, 0, 5])])]
+    pool, width = max(x.k.shape[0] for x in xs), max(len(x.table[0]) for x in xs)
+    q = torch.zeros((80, Hq, 128), dtype=dtype, device="cuda")
+    k = torch.zeros((pool, Hkv, 16, 128), dtype=dtype, device="cuda")
+    v, out = torch.zeros_like(k), torch.zeros_like(q)
+    tab, qs, lens = i32([[0] * width] * 3), i32([0] * 4), i32([1] * 3)
+    w = attn_ws(80, Hq, Hkv, dtype)
+    call = lambda: qdk.think_paged_attn(q, k, v, tab, qs, lens, out, w)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for x in xs + xs[:1]:
+        q.copy_(x.q)
+        k[:x.k.shape[0]].copy_(x.k)
+        v[:x.k.shape[0]].copy_(x.v)
+        tab.fill_(-1)
+        tab[:, :len(x.table[0])] = i32(x.table)
+        qs.copy_(i32(x.q_start))
+        lens.copy_(i32(x.lens))
+        out.fill_(9.0)
+        g.replay()
+        assert torch.equal(out, run_attn(x, Hq, Hkv))
+
+
+# ------------------------------------------------------------------ page gather --
+
+@pytest.mark.parametrize("dtype,page,layout,lens,N", [
+    (BF, 16, "hnd", [1], 1), (BF, 64, "nhd", [1000, 0, 333], 1000), (F32, 48, "hnd", [97, 500], 301), (F32, 256, "nhd", [700], 900)])
+def test_gather_pages(dtype, page, layout, lens, N):
+    x = P.Batch([0] * len(lens), lens, 3, 3, page, dtype, N, layout=layout)
+    want = torch.zeros((len(lens), 3, N, 128), dtype=dtype)
+    for b, n in enumerate(lens):
+        for j in range(min(n, N)):
+            want[b, :, j] = x.k[x.table[b][j // page], :, j % page]
+    canary = torch.full((want.numel() + 256,), 5.0, dtype=dtype, device="cuda")
+    out = canary[128:-128].view(want.shape)
+    qdk.think_gather_pages(x.cache(x.k), i32(x.table), i32(x.lens), out)
+    assert torch.equal(out.cpu(), want)
+    assert (canary[:128] == 5.0).all() and (canary[-128:] == 5.0).all()
+
+
+def test_gather_bad_pages_and_lengths_give_zeros():
+    x = P.Batch([0, 0], [40, 40], 2, 2, 16, BF, 1, poison=False)
+    x.table[0][1], x.table[1][0] = -3, x.k.shape[0]
+    out = torch.full((2, 2, 100, 128), 9.0, dtype=BF, device="cuda")
+    qdk.think_gather_pages(x.cache(x.k), i32(x.table), i32([-5, 2 ** 31 - 1]), out)
+    assert not out[0].any()
+    assert not out[1, :, :16].any() and torch.equal(out[1, :, 16:40].cpu(), torch.cat(
+        [x.k[x.table[1][1]], x.k[x.table[1][2]][:, :8]], 1))
+    assert not out[1, :, len(x.table[0]) * 16:].any()
+
+
+# ------------------------------------------------------------------ streams --
+
+def test_two_streams_at_once():
+    xs = [P.Batch([50, 1], [400, 1500], 8, 2, 16, BF, 30 + i) for i in range(2)]
+    want = [run_attn(x, 8, 2) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    args = [(x.q.cuda(), x.cache(x.k), x.cache(x.v), i32(x.table), i32(x.q_start), i32(x.lens), torch.zeros_like(o),
+             attn_ws(x.T, 8, 2, BF)) for x, o in zip(xs, want)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, a in zip(streams, args):
+            qdk.think_paged_attn(*a, stream=s)
+    torch.cuda.synchronize()
+    for a, o in zip(args, want):
+        assert torch.equal(a[6], o)
