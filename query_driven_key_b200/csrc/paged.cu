@@ -11,6 +11,7 @@
 #include "host.cuh"
 #include "paged_plan.cuh"
 #include "paged_simt.cuh"
+#include "paged_tc.cuh"
 #include "pages.cuh"
 #include "rope.cuh"
 #include "think.h"
@@ -46,36 +47,56 @@ think_status_t check_table(const int32_t *table, int64_t table_ld, int max_block
 struct PagedPlan {
     int rows;      // query rows of an item
     int parts;     // blocks
+    int sides;     // partials of a piece
     int rows_cap;  // rows of a partial
-    size_t smem;
+    size_t smem, ws_bytes;
 };
 
-// fp32: items of 64 query rows (two blocks an SM), or of 16 where no request
-// has more rows than that.
-PagedPlan plan_paged(int64_t T, int G, int max_new)
+// bf16: items of 256 query rows, a block an SM.  fp32: items of 64 query rows,
+// two blocks an SM, or of 16 where no request has more rows than that.
+PagedPlan plan_paged(think_dtype_t dtype, int64_t T, int G, int max_new)
 {
     PagedPlan p;
-    p.rows = (int64_t)max_new * G <= 16 ? 16 : 64;
-    p.parts = kTargetSMs * 2;
-    p.smem = p.rows == 16 ? paged_simt_smem<16>() : paged_simt_smem<64>();
-    p.rows_cap = (int)std::min<int64_t>(64, T * G);
+    if (dtype == THINK_BF16) {
+        p.rows = kPtRows;
+        p.parts = kTargetSMs;
+        p.sides = 2;
+        p.smem = paged_tc_smem();
+    } else {
+        p.rows = (int64_t)max_new * G <= 16 ? 16 : 64;
+        p.parts = kTargetSMs * 2;
+        p.sides = 1;
+        p.smem = p.rows == 16 ? paged_simt_smem<16>() : paged_simt_smem<64>();
+    }
+    // (the same for 16 and 64 rows, so that max_new does not change the workspace)
+    p.rows_cap = (int)std::min<int64_t>(dtype == THINK_BF16 ? 128 : 64, T * G);
+    p.ws_bytes = kPagedHeader + sizeof(float) * (size_t)p.parts * 2 * p.sides * (size_t)p.rows_cap * kPartLd;
     return p;
 }
 
-size_t paged_ws_bytes(int64_t T, int G)
-{
-    const int64_t rows = std::min<int64_t>(128, T * G);
-    return kPagedHeader + sizeof(float) * (size_t)kTargetSMs * 2 * 4 * (size_t)rows * kPartLd;
-}
-
-template <typename T, int R>
+template <int R>
 think_status_t launch_paged_simt(const PagedArgs &a, const PagedPlan &p, cudaStream_t st)
 {
-    const void *kern = reinterpret_cast<const void *>(&paged_simt_kernel<T, R>);
-    if (!ensure_smem(kern, p.smem)) return THINK_ERR_CUDA;
-    const think_status_t rc = launch_pdl(paged_simt_kernel<T, R>, dim3((unsigned)p.parts), dim3(kSimtThreads), p.smem, st, a);
+    if (!ensure_smem(reinterpret_cast<const void *>(&paged_simt_kernel<R>), p.smem)) return THINK_ERR_CUDA;
+    const think_status_t rc = launch_pdl(paged_simt_kernel<R>, dim3((unsigned)p.parts), dim3(kSimtThreads), p.smem, st, a);
     if (rc != THINK_OK) return rc;
-    return launch_pdl(paged_merge_kernel<T, R, kSimtBN, false>, dim3((unsigned)(p.parts - 1), kMergeSlices),
+    return launch_pdl(paged_merge_kernel<float, R, kSimtBN, false>, dim3((unsigned)(p.parts - 1), kMergeSlices),
+                      dim3(kMergeThreads), 0, st, a);
+}
+
+think_status_t launch_paged_tc(const PagedArgs &a, const PagedPlan &p, cudaStream_t st)
+{
+    // rows of one TMA load: the largest power of two that divides the page, at most a tile
+    const int chunk = std::min(kPtBN, a.page_size & -a.page_size);
+    CUtensorMap mk, mv;
+    if (!make_map_4d(&mk, THINK_BF16, a.k, kD, a.page_size, a.Hkv, a.num_pages, a.k_sn, a.k_sh, a.k_sp, 64, chunk, true) ||
+        !make_map_4d(&mv, THINK_BF16, a.v, kD, a.page_size, a.Hkv, a.num_pages, a.v_sn, a.v_sh, a.v_sp, 64, chunk, true))
+        return THINK_ERR_CUDA;
+    if (!ensure_smem(reinterpret_cast<const void *>(&paged_tc_kernel), p.smem)) return THINK_ERR_CUDA;
+    const think_status_t rc =
+        launch_pdl(paged_tc_kernel, dim3((unsigned)p.parts), dim3(kPtThreads), p.smem, st, mk, mv, a, chunk);
+    if (rc != THINK_OK) return rc;
+    return launch_pdl(paged_merge_kernel<__nv_bfloat16, kPtRows, kPtBN, true>, dim3((unsigned)(p.parts - 1), kMergeSlices),
                       dim3(kMergeThreads), 0, st, a);
 }
 
@@ -187,7 +208,7 @@ think_status_t think_norm_rope_append(const void *q, const int64_t q_strides[2],
 size_t think_paged_attn_workspace_size(int64_t T, int Hq, int Hkv, int d, think_dtype_t dtype)
 {
     if (T < 0 || Hkv <= 0 || Hq < Hkv || Hq % Hkv != 0 || d != kD || !dtype_ok(dtype)) return 0;
-    return paged_ws_bytes(T, Hq / Hkv);
+    return plan_paged(dtype, T, Hq / Hkv, 1).ws_bytes;
 }
 
 think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const void *k_cache,
@@ -213,25 +234,30 @@ think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const
         !aligned4(q_start) || !aligned4(kv_lens) || !strides16(q_strides, 2, es) || !strides16(out_strides, 2, es) ||
         !strides16(k_cache_strides, 3, es) || !strides16(v_cache_strides, 3, es))
         return THINK_ERR_ALIGNMENT;
-    if (workspace_bytes < paged_ws_bytes(T, G)) return THINK_ERR_WORKSPACE;
-    const PagedPlan p = plan_paged(T, G, max_new > 0 ? (int)std::min<int64_t>(max_new, T) : (int)T);
+    for (const int64_t *c : {k_cache_strides, v_cache_strides})  // TMA: strides above 0 and below 2^40 bytes
+        for (int i = 0; i < 3; ++i) {
+            if (c[i] == 0 && (i == 0 ? num_pages : i == 1 ? Hkv : page_size) > 1) return THINK_ERR_INVALID_ARG;
+            if (c[i] >= ((int64_t)1 << 40) / (int64_t)es) return THINK_ERR_UNSUPPORTED;
+        }
+    const PagedPlan p = plan_paged(dtype, T, G, max_new > 0 ? (int)std::min<int64_t>(max_new, T) : (int)T);
+    if (workspace_bytes < p.ws_bytes) return THINK_ERR_WORKSPACE;
     PagedArgs a = {};
     a.q = q, a.k = k_cache, a.v = v_cache, a.out = out;
     a.q_start = q_start, a.kv_lens = kv_lens, a.table = block_table;
     a.status = static_cast<unsigned *>(workspace);
     a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + kPagedHeader);
     a.q_st = q_strides[0], a.q_sh = q_strides[1], a.o_st = out_strides[0], a.o_sh = out_strides[1];
-    a.k_sp = k_cache_strides[0], a.k_sh = k_cache_strides[1], a.k_sn = k_cache_strides[2];
-    a.v_sp = v_cache_strides[0], a.v_sh = v_cache_strides[1], a.v_sn = v_cache_strides[2];
+    // the stride of a dimension of one element is free
+    a.k_sp = num_pages > 1 ? k_cache_strides[0] : kD, a.k_sh = Hkv > 1 ? k_cache_strides[1] : kD, a.k_sn = k_cache_strides[2];
+    a.v_sp = num_pages > 1 ? v_cache_strides[0] : kD, a.v_sh = Hkv > 1 ? v_cache_strides[1] : kD, a.v_sn = v_cache_strides[2];
     a.table_ld = table_ld;
     a.B = B, a.T = (int)T, a.Hkv = Hkv, a.G = G;
     a.page_size = page_size, a.num_pages = num_pages, a.limit = max_blocks * page_size, a.window = window;
-    a.rows_cap = p.rows_cap, a.parts = p.parts;
+    a.rows_cap = p.rows_cap, a.parts = p.parts, a.sides = p.sides;
     a.scale_log2 = scale * 1.44269504088896341f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == THINK_BF16)
-        return p.rows == 16 ? launch_paged_simt<__nv_bfloat16, 16>(a, p, st) : launch_paged_simt<__nv_bfloat16, 64>(a, p, st);
-    return p.rows == 16 ? launch_paged_simt<float, 16>(a, p, st) : launch_paged_simt<float, 64>(a, p, st);
+    if (dtype == THINK_BF16) return launch_paged_tc(a, p, st);
+    return p.rows == 16 ? launch_paged_simt<16>(a, p, st) : launch_paged_simt<64>(a, p, st);
 }
 
 think_status_t think_gather_pages(const void *cache, const int64_t cache_strides[3], int num_pages, int page_size,

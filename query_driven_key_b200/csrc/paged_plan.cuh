@@ -25,13 +25,14 @@ struct PagedArgs {
     void *out;
     const int32_t *q_start, *kv_lens, *table;
     unsigned *status;
-    float *part;  // [blocks][2 pieces][2 sides][rows_cap][kPartLd]
+    float *part;  // [parts][2 pieces][sides][rows_cap][kPartLd]
     int64_t q_st, q_sh, o_st, o_sh;
     int64_t k_sp, k_sh, k_sn, v_sp, v_sh, v_sn;
     int64_t table_ld;
     int B, T, Hkv, G, page_size, num_pages, limit, window;
     int rows_cap;  // rows of a partial that may hold data
     int parts;     // blocks of the attention launch
+    int sides;     // partials of a piece: 2 where two warpgroups work on it
     float scale_log2;
 };
 
@@ -201,6 +202,10 @@ struct Walk {
         whole = head && j1 == t.j1;
     }
     __device__ __forceinline__ bool live() const { return left > 0; }
+    __device__ __forceinline__ void assign(const Walk &o)
+    {
+        p = o.p, s = o.s, left = o.left, t = o.t, j0 = o.j0, j1 = o.j1, whole = o.whole, head = o.head;
+    }
     __device__ __forceinline__ void next()
     {
         left -= j1 - j0;
@@ -228,7 +233,7 @@ struct Walk {
 // block's work on the piece, where it has two).
 __device__ __forceinline__ float *part_at(const PagedArgs &a, int part, int piece, int side)
 {
-    return a.part + ((int64_t)((part * 2 + piece) * 2 + side)) * a.rows_cap * kPartLd;
+    return a.part + ((int64_t)((part * 2 + piece) * a.sides + side)) * a.rows_cap * kPartLd;
 }
 
 template <typename T>

@@ -1,5 +1,5 @@
-// paged_simt.cuh -- attention of new tokens over the paged cache on the CUDA
-// cores (the plan: paged_plan.cuh).
+// paged_simt.cuh -- attention of new tokens over the paged cache in fp32, on
+// the CUDA cores (the plan: paged_plan.cuh).
 //
 // Per item, over its key tiles of BN = 64, with running maxima m and sums l
 // (fp32, logarithms to base 2):
@@ -24,19 +24,7 @@ constexpr size_t paged_simt_smem()
     return sizeof(float) * ((size_t)R * kD + 2 * (size_t)kSimtBN * kD + (size_t)kSimtBN * R);
 }
 
-template <typename T>
-__device__ __forceinline__ float4 load_row4(const T *p);
-template <>
-__device__ __forceinline__ float4 load_row4<float>(const float *p)
-{
-    return __ldg(reinterpret_cast<const float4 *>(p));
-}
-template <>
-__device__ __forceinline__ float4 load_row4<__nv_bfloat16>(const __nv_bfloat16 *p)
-{
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
-    return make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
-}
+__device__ __forceinline__ float4 load_row4(const float *p) { return __ldg(reinterpret_cast<const float4 *>(p)); }
 
 // Element 4 c4 of row n of a 128-wide fp32 tile whose 16-byte vectors are
 // permuted within 8 rows, so that 8 rows' equal columns lie in 8 bank groups.
@@ -44,7 +32,7 @@ __device__ __forceinline__ int swz(int n, int c4) { return n * kD + ((c4 ^ (n & 
 
 // Thread (tx, ty) = (tid % 16, tid / 16) holds rows ty + 16 i and, of the
 // logits, tokens tx + 16 j, of the output channels 4 tx + 64 jj.
-template <typename T, int R>
+template <int R>
 __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedArgs a)
 {
     constexpr int BN = kSimtBN, MI = R / 16;
@@ -67,7 +55,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedArg
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
                 const int gr = w.p.qt * R + r;
-                x = load_row4(static_cast<const T *>(a.q) + (int64_t)(w.s.row0 + gr / a.G) * a.q_st +
+                x = load_row4(static_cast<const float *>(a.q) + (int64_t)(w.s.row0 + gr / a.G) * a.q_st +
                               (int64_t)(w.p.h * a.G + gr % a.G) * a.q_sh + 4 * c4);
             }
             *reinterpret_cast<float4 *>(qs + r * kD + 4 * c4) = x;
@@ -92,8 +80,8 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedArg
                     const int page = a.table[(int64_t)w.p.b * a.table_ld + j];
                     if ((unsigned)page < (unsigned)a.num_pages) {
                         const int64_t off = key - (int64_t)j * a.page_size;
-                        x = load_row4(static_cast<const T *>(a.k) + page * a.k_sp + w.p.h * a.k_sh + off * a.k_sn + 4 * c4);
-                        y = load_row4(static_cast<const T *>(a.v) + page * a.v_sp + w.p.h * a.v_sh + off * a.v_sn + 4 * c4);
+                        x = load_row4(static_cast<const float *>(a.k) + page * a.k_sp + w.p.h * a.k_sh + off * a.k_sn + 4 * c4);
+                        y = load_row4(static_cast<const float *>(a.v) + page * a.v_sp + w.p.h * a.v_sh + off * a.v_sn + 4 * c4);
                     } else if (c4 == 0) {
                         atomicOr(a.status, THINK_DEVICE_BAD_PAGE);
                     }
@@ -169,7 +157,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedArg
             if (w.whole) {
                 const float inv = s > 0.f ? 1.f / s : 0.f;
                 const int gr = w.p.qt * R + r;
-                T *dst = static_cast<T *>(a.out) + (int64_t)(w.s.row0 + gr / a.G) * a.o_st +
+                float *dst = static_cast<float *>(a.out) + (int64_t)(w.s.row0 + gr / a.G) * a.o_st +
                          (int64_t)(w.p.h * a.G + gr % a.G) * a.o_sh + 4 * tx;
                 store_out4(dst, make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv));
                 store_out4(dst + 64, make_float4(o[i][4] * inv, o[i][5] * inv, o[i][6] * inv, o[i][7] * inv));
