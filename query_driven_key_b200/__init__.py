@@ -12,6 +12,7 @@ importing this package raises if ``libthink.so`` cannot be loaded.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -142,6 +143,22 @@ def _load() -> ctypes.CDLL:
 
 
 lib = _load()
+
+
+def _load_binding():
+    """The module that marshals the paged calls, bound to the loaded library's entry points."""
+    path = os.path.join(_PKG, "_binding.so")
+    if not os.path.exists(path):
+        raise ImportError(f"_binding.so not found at {path}; build it with `python query_driven_key_b200/build.py`")
+    spec = importlib.util.spec_from_file_location("query_driven_key_b200._binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(*(ctypes.cast(getattr(lib, "think_" + f), ctypes.c_void_p).value
+                  for f in ("extend_pages", "norm_rope_append", "paged_attn", "gather_pages")))
+    return module
+
+
+_binding = _load_binding()
 
 
 class ThinkError(RuntimeError):
@@ -508,60 +525,12 @@ class EvictedCache:
 
 # ------------------------------------------------------------ paged cache --
 
-def _on(where: str, *tensors):
-    """The device of the tensors (None skipped), which must all lie on it."""
-    device = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda or (device is not None and t.device != device):
-            raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: every tensor must lie on one GPU")
-        device = t.device
-    return device
-
-
-def _call(where: str, device, stream, fn, *args) -> None:
-    """Call a C entry point with `device` current, on `stream` (default: the
-    device's current stream)."""
-    index = device.index
-    raw = _raw_stream(index) if stream is None else stream.cuda_stream
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, raw)
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, raw)
-    if rc != THINK_OK:
-        raise ThinkError(rc, where)
-
-
-def _i64x(*xs):
-    return (ctypes.c_int64 * len(xs))(*xs)
-
-
-def _rows(where: str, t: torch.Tensor):
-    """Token and head strides of a [T,H,d] tensor with contiguous channels."""
-    if t.dim() != 3 or t.stride(2) != 1:
-        raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: expected a [T,H,d] tensor with contiguous channels")
-    return _i64x(t.stride(0), t.stride(1))
-
-
-def _pool(where: str, t: torch.Tensor):
-    """Page, head and row strides of a [pages,Hkv,page_size,d] tensor."""
-    if t.dim() != 4 or t.stride(3) != 1:
-        raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: expected a [pages,Hkv,page_size,d] tensor with contiguous channels")
-    return _i64x(t.stride(0), t.stride(1), t.stride(2))
-
-
-def _ints(where: str, dtype: torch.dtype, n: int, *tensors) -> None:
-    for t in tensors:
-        if t.dtype != dtype or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-            raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: expected contiguous {dtype} tensors of {n} elements")
-
-
-def _table(where: str, t: torch.Tensor, B: int) -> int:
-    if t.dtype != torch.int32 or t.dim() != 2 or t.shape[0] != B or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: expected a [{B},max_blocks] int32 block table")
-    return t.stride(0) if B > 1 else max(t.stride(0), t.shape[1])
+def _paged(where: str, answer) -> None:
+    """Raise for a call of the binding that was not made: a status code, or the reason in words."""
+    if answer is not None:
+        if isinstance(answer, str):
+            raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: {answer}")
+        raise ThinkError(answer, where)
 
 
 def think_extend_pages_workspace_size() -> int:
@@ -574,21 +543,10 @@ def think_extend_pages(new_lens: torch.Tensor, kv_lens: torch.Tensor, block_tabl
                        slots: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
     """new_lens, kv_lens [B], block_table [B,max_blocks], the stack free_pages with its height free_count [1] (int32)
     -> kv_lens_out [B], free_count_out [1], q_start [B+1], positions [T] (int32), slots [T] (int64), fresh table entries."""
-    where = "think_extend_pages"
-    B, T = new_lens.shape[0], positions.shape[0]
-    device = _on(where, new_lens, kv_lens, block_table, free_pages, free_count, kv_lens_out, free_count_out, q_start,
-                 positions, slots, workspace)
-    _ints(where, torch.int32, B, new_lens, kv_lens, kv_lens_out)
-    _ints(where, torch.int32, 1, free_count, free_count_out)
-    _ints(where, torch.int32, B + 1, q_start)
-    _ints(where, torch.int32, T, positions)
-    _ints(where, torch.int64, T, slots)
-    _ints(where, torch.int32, free_pages.numel(), free_pages)
-    ld = _table(where, block_table, B)
-    _call(where, device, stream, lib.think_extend_pages, new_lens.data_ptr(), kv_lens.data_ptr(), B, int(page_size),
-          block_table.data_ptr(), ld, block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0],
-          free_count.data_ptr(), T, kv_lens_out.data_ptr(), free_count_out.data_ptr(), q_start.data_ptr(),
-          positions.data_ptr(), slots.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    answer = _binding.extend_pages(new_lens, kv_lens, block_table, free_pages, free_count, page_size, kv_lens_out,
+                                   free_count_out, q_start, positions, slots, workspace, stream)
+    if answer is not None:
+        _paged("think_extend_pages", answer)
 
 
 def think_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_weight: torch.Tensor | None,
@@ -597,31 +555,14 @@ def think_norm_rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, q_
                            v_cache: torch.Tensor, stream=None) -> None:
     """q [T,Hq,d], k, v [T,Hkv,d] -> q_out [T,Hq,d] (normed, turned) and the rows `slots` [T] int64 of k_cache, v_cache
     [pages,Hkv,page_size,d] (k normed and turned).  inv_freq [rot/2] fp64 (None: no rotation), positions [T] int32."""
-    where = "think_norm_rope_append"
-    T, Hq, d = q.shape
-    Hkv = k.shape[1]
-    device = _on(where, q, k, v, q_weight, k_weight, inv_freq, positions, slots, q_out, k_cache, v_cache)
-    _ints(where, torch.int32, T, positions)
-    _ints(where, torch.int64, T, slots)
-    if inv_freq is not None:
-        _ints(where, torch.float64, inv_freq.numel(), inv_freq)
-    for w in (q_weight, k_weight):
-        if w is not None:
-            _ints(where, q.dtype, d, w)
-    if any(t.dtype != q.dtype for t in (k, v, q_out, k_cache, v_cache)) or k.shape != (T, Hkv, d) or v.shape != k.shape \
-            or q_out.shape != q.shape or k_cache.shape[1] != Hkv or k_cache.shape[3] != d or v_cache.shape != k_cache.shape:
-        raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: shapes or dtypes do not match")
-    _call(where, device, stream, lib.think_norm_rope_append, q.data_ptr(), _rows(where, q), k.data_ptr(), _rows(where, k),
-          v.data_ptr(), _rows(where, v), T, Hq, Hkv, d, _dtype(q), None if q_weight is None else q_weight.data_ptr(),
-          None if k_weight is None else k_weight.data_ptr(), float(eps),
-          None if inv_freq is None else inv_freq.data_ptr(), 0 if inv_freq is None else 2 * inv_freq.shape[0],
-          int(bool(neighbours)), positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(), _rows(where, q_out),
-          k_cache.data_ptr(), _pool(where, k_cache), v_cache.data_ptr(), _pool(where, v_cache), k_cache.shape[0],
-          k_cache.shape[2])
+    answer = _binding.norm_rope_append(q, k, v, q_weight, k_weight, eps, inv_freq, neighbours, positions, slots, q_out,
+                                       k_cache, v_cache, stream)
+    if answer is not None:
+        _paged("think_norm_rope_append", answer)
 
 
 def think_paged_attn_workspace_size(T: int, Hq: int, Hkv: int, d: int = 128, dtype: torch.dtype = torch.bfloat16) -> int:
-    return lib.think_paged_attn_workspace_size(int(T), Hq, Hkv, d, THINK_BF16 if dtype == torch.bfloat16 else THINK_F32)
+    return lib.think_paged_attn_workspace_size(T, Hq, Hkv, d, THINK_BF16 if dtype == torch.bfloat16 else THINK_F32)
 
 
 def think_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -630,39 +571,19 @@ def think_paged_attn(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tens
     """q [T,Hq,d], caches [pages,Hkv,page_size,d], block_table [B,max_blocks], q_start [B+1], kv_lens [B] (int32, with the
     new tokens) -> out [T,Hq,d] of q's dtype: causal attention of the new tokens, with window > 0 over the last
     `window` keys.  max_new: the largest number of new tokens of a request (0: not known)."""
-    where = "think_paged_attn"
-    T, Hq, d = q.shape
-    pages, Hkv, page_size, dk = k_cache.shape
-    B = kv_lens.shape[0]
-    device = _on(where, q, k_cache, v_cache, block_table, q_start, kv_lens, out, workspace)
-    _ints(where, torch.int32, B, kv_lens)
-    _ints(where, torch.int32, B + 1, q_start)
-    if any(t.dtype != q.dtype for t in (k_cache, v_cache, out)) or v_cache.shape != k_cache.shape or dk != d \
-            or out.shape != q.shape:
-        raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: shapes or dtypes do not match")
-    ld = _table(where, block_table, B)
-    _call(where, device, stream, lib.think_paged_attn, q.data_ptr(), _rows(where, q), k_cache.data_ptr(),
-          _pool(where, k_cache), v_cache.data_ptr(), _pool(where, v_cache), pages, page_size, block_table.data_ptr(), ld,
-          block_table.shape[1], q_start.data_ptr(), kv_lens.data_ptr(), B, T, int(max_new), Hq, Hkv, d, _dtype(q),
-          float(1.0 / float(d) ** 0.5 if scale is None else scale), int(window), out.data_ptr(), _rows(where, out),
-          workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    answer = _binding.paged_attn(q, k_cache, v_cache, block_table, q_start, kv_lens, out, workspace, window, scale, max_new,
+                                 stream)
+    if answer is not None:
+        _paged("think_paged_attn", answer)
 
 
 def think_gather_pages(cache: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor, out: torch.Tensor,
                        stream=None) -> None:
     """cache [pages,Hkv,page_size,d], block_table [B,max_blocks], kv_lens [B] (int32) -> out [B,Hkv,N,d] (contiguous),
     zeros behind a request's length."""
-    where = "think_gather_pages"
-    pages, Hkv, page_size, d = cache.shape
-    B = kv_lens.shape[0]
-    device = _on(where, cache, block_table, kv_lens, out)
-    _ints(where, torch.int32, B, kv_lens)
-    if out.dtype != cache.dtype or not out.is_contiguous() or out.dim() != 4 or out.shape[:2] != (B, Hkv) or out.shape[3] != d:
-        raise ThinkError(THINK_ERR_INVALID_ARG, f"{where}: out must be a contiguous [B,Hkv,N,d] tensor of the cache's dtype")
-    ld = _table(where, block_table, B)
-    _call(where, device, stream, lib.think_gather_pages, cache.data_ptr(), _pool(where, cache), pages, page_size,
-          block_table.data_ptr(), ld, block_table.shape[1], kv_lens.data_ptr(), B, Hkv, out.shape[2], d, _dtype(cache),
-          out.data_ptr())
+    answer = _binding.gather_pages(cache, block_table, kv_lens, out, stream)
+    if answer is not None:
+        _paged("think_gather_pages", answer)
 
 
 def think_workspace_init(workspace: torch.Tensor, stream=None) -> None:

@@ -100,11 +100,23 @@ think_status_t launch_paged_tc(const PagedArgs &a, const PagedPlan &p, cudaStrea
                       dim3(kMergeThreads), 0, st, a);
 }
 
-template <typename T>
-think_status_t launch_rope(bool neighbours, int64_t rows, const RopeArgs &a, cudaStream_t st)
+template <typename T, bool NEIGHBOURS>
+think_status_t launch_rope_n(const RopeArgs &a, cudaStream_t st)
 {
-    return neighbours ? launch_pdl(norm_rope_append_kernel<T, true>, dim3((unsigned)rows), dim3(kRopeThreads), 0, st, a)
-                      : launch_pdl(norm_rope_append_kernel<T, false>, dim3((unsigned)rows), dim3(kRopeThreads), 0, st, a);
+    // a block holds up to 4 head rows a group of 16 (bf16) or 32 (fp32) lanes; more heads are shared between blocks
+    const int groups = kRopeThreads * 16 / (kD * (int)sizeof(T));
+    const int64_t rows = a.Hq + 2 * (int64_t)a.Hkv, shares = ceil_div(rows, groups * kRopeUnroll);
+    const size_t smem = (size_t)kRopeStages * (size_t)ceil_div(ceil_div(rows, shares), groups) * kRopeThreads * 16;
+    auto kern = norm_rope_append_kernel<T, NEIGHBOURS>;
+    if (!ensure_smem(reinterpret_cast<const void *>(kern), smem)) return THINK_ERR_CUDA;
+    const int64_t blocks = std::min(a.T, std::max<int64_t>(1, kTargetSMs * kRopeBlocksPerSM / shares));
+    return launch_pdl(kern, dim3((unsigned)blocks, (unsigned)shares), dim3(kRopeThreads), smem, st, a);
+}
+
+template <typename T>
+think_status_t launch_rope(bool neighbours, const RopeArgs &a, cudaStream_t st)
+{
+    return neighbours ? launch_rope_n<T, true>(a, st) : launch_rope_n<T, false>(a, st);
 }
 
 }  // namespace
@@ -199,10 +211,11 @@ think_status_t think_norm_rope_append(const void *q, const int64_t q_strides[2],
         a.vc_sp = v_cache_strides[0], a.vc_sh = v_cache_strides[1], a.vc_sn = v_cache_strides[2];
     }
     a.num_slots = (int64_t)num_pages * page_size;
+    a.T = T;
     a.Hq = Hq, a.Hkv = Hkv, a.rot = rot, a.page_size = page_size;
     a.eps = eps;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return dtype == THINK_BF16 ? launch_rope<__nv_bfloat16>(neighbours != 0, T, a, st) : launch_rope<float>(neighbours != 0, T, a, st);
+    return dtype == THINK_BF16 ? launch_rope<__nv_bfloat16>(neighbours != 0, a, st) : launch_rope<float>(neighbours != 0, a, st);
 }
 
 size_t think_paged_attn_workspace_size(int64_t T, int Hq, int Hkv, int d, think_dtype_t dtype)

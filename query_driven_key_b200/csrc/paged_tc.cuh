@@ -56,29 +56,6 @@ struct PtBars {
 
 constexpr size_t paged_tc_smem() { return 1024u + (2u + kPtStages) * (size_t)kPtTile; }
 
-__device__ __forceinline__ uint64_t pack2(float lo, float hi)
-{
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
-__device__ __forceinline__ void unpack2(uint64_t d, float &lo, float &hi)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // One item's shape for the block's roles.
 struct PtItem {
     int rows;    // query rows
@@ -472,10 +449,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll
                 for (int c = 0; c < 32; c += 8)
                     *reinterpret_cast<uint4 *>(dst + 32 * i + c) =
-                        make_uint4(RopeVec<__nv_bfloat16>::two(o[c] * f, o[c + 1] * f),
-                                   RopeVec<__nv_bfloat16>::two(o[c + 2] * f, o[c + 3] * f),
-                                   RopeVec<__nv_bfloat16>::two(o[c + 4] * f, o[c + 5] * f),
-                                   RopeVec<__nv_bfloat16>::two(o[c + 6] * f, o[c + 7] * f));
+                        make_uint4(bf16_pair(o[c] * f, o[c + 1] * f),
+                                   bf16_pair(o[c + 2] * f, o[c + 3] * f),
+                                   bf16_pair(o[c + 4] * f, o[c + 5] * f),
+                                   bf16_pair(o[c + 6] * f, o[c + 7] * f));
             };
             if (join) {
                 // warpgroup 1 hands its state over in the unused second Q tile,

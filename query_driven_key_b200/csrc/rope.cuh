@@ -7,22 +7,30 @@
 //     (x1, x2) -> (x1 cos a - x2 sin a, x2 cos a + x1 sin a),
 // pairs (i, i + rot/2) or (2i, 2i + 1).  Values are copied.
 //
-// Bound by HBM: every head row is read once and written once.  One block a
-// token; a lane holds 16 bytes of a head row, so that 16 (bf16) or 32 (fp32)
-// lanes hold a row and the norm is a shuffle reduction.  The block's rows are
-// loaded into registers first, so that the loads run while its first threads
-// turn the position into the token's cosines and sines (shared by its heads).
-// The angle is formed and reduced in fp64: at position 131072 an fp32 product
-// is off by up to 2^-24 * 131072 = 0.008 rad.  All arithmetic after it is fp32,
-// with one rounding at the store.
+// Bound by HBM: every head row is read once and written once.  Persistent
+// blocks take runs of tokens; the threads copy the head rows of the next tokens
+// (up to 16 KB each) to shared memory ahead with cp.async, which holds no
+// registers.  16 (bf16) or 32 (fp32) lanes of a warp share a row, and each
+// reads back two 8-byte chunks chosen so that it holds both partners of its
+// pairs; only the norm is a shuffle reduction.  With the weights folded into a
+// token's factors (y = rsqrt(..) * (x * cos w + partner * (-+ sin) w')) a row
+// costs a few packed fp32 operations a lane.  Rows of one warp are its own
+// copies, so that the steady state has no barrier but the two of a batch of
+// tokens, in which the threads turn positions into factors (one thread a pair;
+// all heads of a token share them).  The angle is formed and reduced in fp64:
+// at position 131072 an fp32 product is off by up to 2^-24 * 131072 = 0.008 rad.
+// All arithmetic after it is fp32, with one rounding at the store.
 #pragma once
 
 #include "ptx.cuh"
 
 namespace think {
 
-constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 4;  // head rows a lane group holds at once
+constexpr int kRopeThreads = 512;
+constexpr int kRopeUnroll = 2;       // head rows of a thread
+constexpr int kRopeStages = 4;       // tokens in shared memory
+constexpr int kRopeBatch = kRopeThreads / (kD / 2);  // tokens whose factors are formed together
+constexpr int kRopeBlocksPerSM = 2;
 
 struct RopeArgs {
     const void *q, *k, *v, *wq, *wk;
@@ -32,144 +40,259 @@ struct RopeArgs {
     const int64_t *slots;
     int64_t q_st, q_sh, k_st, k_sh, v_st, v_sh, qo_st, qo_sh;
     int64_t kc_sp, kc_sh, kc_sn, vc_sp, vc_sh, vc_sn;
-    int64_t num_slots;
+    int64_t num_slots, T;
     int Hq, Hkv, rot, page_size;
     float eps;
 };
 
-template <typename T> struct RopeVec;  // 16 bytes of a row as fp32 channels
-template <> struct RopeVec<__nv_bfloat16> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void unpack(const uint4 w, float x[8])
+__device__ __forceinline__ uint64_t pack2(float lo, float hi)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ void unpack2(uint64_t d, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t swap2(uint64_t a)
+{
+    float lo, hi;
+    unpack2(a, lo, hi);
+    return pack2(hi, lo);
+}
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// An 8-byte chunk of a row as pairs of fp32 channels.
+template <typename T> struct RopeChunk;
+template <> struct RopeChunk<__nv_bfloat16> {
+    static constexpr int N = 4;  // channels
+    static __device__ __forceinline__ void unpack(uint2 w, uint64_t x[2])
     {
-        x[0] = bf16lo(w.x), x[1] = bf16hi(w.x), x[2] = bf16lo(w.y), x[3] = bf16hi(w.y);
-        x[4] = bf16lo(w.z), x[5] = bf16hi(w.z), x[6] = bf16lo(w.w), x[7] = bf16hi(w.w);
+        x[0] = pack2(bf16lo(w.x), bf16hi(w.x)), x[1] = pack2(bf16lo(w.y), bf16hi(w.y));
     }
-    static __device__ __forceinline__ uint32_t two(float lo, float hi)
+    static __device__ __forceinline__ uint2 pack(const uint64_t x[2])
     {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t *>(&p);
-    }
-    static __device__ __forceinline__ uint4 pack(const float x[8])
-    {
-        return make_uint4(two(x[0], x[1]), two(x[2], x[3]), two(x[4], x[5]), two(x[6], x[7]));
+        float a, b, c, d;
+        unpack2(x[0], a, b), unpack2(x[1], c, d);
+        return make_uint2(bf16_pair(a, b), bf16_pair(c, d));
     }
 };
-template <> struct RopeVec<float> {
-    static constexpr int N = 4;
-    static __device__ __forceinline__ void unpack(const uint4 w, float x[4])
+template <> struct RopeChunk<float> {
+    static constexpr int N = 2;
+    static __device__ __forceinline__ void unpack(uint2 w, uint64_t x[1])
     {
-        x[0] = __uint_as_float(w.x), x[1] = __uint_as_float(w.y), x[2] = __uint_as_float(w.z), x[3] = __uint_as_float(w.w);
+        x[0] = pack2(__uint_as_float(w.x), __uint_as_float(w.y));
     }
-    static __device__ __forceinline__ uint4 pack(const float x[4])
+    static __device__ __forceinline__ uint2 pack(const uint64_t x[1])
     {
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+        float a, b;
+        unpack2(x[0], a, b);
+        return make_uint2(__float_as_uint(a), __float_as_uint(b));
     }
 };
 
+// Rows of a block: blockIdx.y's share of the q, k and v heads (at most UNIT),
+// of the tokens [T x / X, T (x + 1) / X), x = blockIdx.x of X.  Row slot i of a
+// thread is a fixed head, so that its addresses only move with the token.
 template <typename T, bool NEIGHBOURS>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_append_kernel(const RopeArgs a)
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSM) norm_rope_append_kernel(const RopeArgs a)
 {
-    constexpr int VEC = RopeVec<T>::N;
-    constexpr int LANES = kD / VEC;             // lanes of a head row
+    constexpr int CH = RopeChunk<T>::N;           // channels of a chunk
+    constexpr int VEC = 2 * CH;                   // channels of a lane
+    constexpr int LANES = kD / VEC;               // lanes of a head row
     constexpr int GROUPS = kRopeThreads / LANES;  // head rows at once
-    __shared__ float2 s_cs[kD / 2];
-    const int64_t t = blockIdx.x;
-    const int tid = threadIdx.x;
-    const int lane = tid % LANES, grp = tid / LANES;
-    const int c = lane * VEC;
-    const int rows = a.Hq + 2 * a.Hkv;
+    constexpr int P = CH / 2;                     // fp32 pairs of a chunk
+    extern __shared__ unsigned char ring[];       // [stages][row slots][threads][16 B]
+    // per token of the batch, rows of q or k, and lane: what its first chunk's and its second chunk's channels
+    // are multiplied by, then what their partners are
+    __shared__ float4 s_f[kRopeBatch][2][VEC / 2][LANES];
+    __shared__ int64_t s_off[kRopeBatch][4];  // the token's row in q_out, the key and the value pool, -1: none
+    const int tid = threadIdx.x, lane = tid % LANES, grp = tid / LANES;
+    const int rows = a.Hq + 2 * a.Hkv, half = a.rot / 2;
+    const int row0 = (int)((int64_t)rows * blockIdx.y / gridDim.y), row1 = (int)((int64_t)rows * (blockIdx.y + 1) / gridDim.y);
+    const int64_t t0 = a.T * blockIdx.x / gridDim.x, t1 = a.T * (blockIdx.x + 1) / gridDim.x;
+    const uint32_t stage_bytes = (uint32_t)((row1 - row0 + GROUPS - 1) / GROUPS) * (kRopeThreads * 16);
+    // This lane's chunks: channels a0 .. and b0 .., each the other's partners
+    // (NEIGHBOURS: partners lie beside each other); lanes past the turned
+    // channels hold neighbouring chunks of the rest.
+    const int turning = NEIGHBOURS ? 0 : half / CH;
+    const int a0 = NEIGHBOURS ? lane * VEC : lane < turning ? lane * CH : a.rot + (lane - turning) * VEC;
+    const int b0 = !NEIGHBOURS && lane < turning ? a0 + half : a0 + CH;
+    const unsigned char *src[kRopeUnroll];  // the next token's vector of this thread
+    int64_t step[kRopeUnroll];              // bytes to the token after it
+    T *dst[kRopeUnroll];                    // the head's row but for s_off
+    int kind[kRopeUnroll];                  // 0 q, 1 k, 2 v, 3 none
+#pragma unroll
+    for (int i = 0; i < kRopeUnroll; ++i) {
+        const int r = row0 + grp + i * GROUPS;
+        kind[i] = r >= row1 ? 3 : r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;
+        const int h = r - (kind[i] == 0 ? 0 : kind[i] == 1 ? a.Hq : a.Hq + a.Hkv);
+        const void *p = kind[i] == 0 ? a.q : kind[i] == 1 ? a.k : a.v;
+        const int64_t st = kind[i] == 0 ? a.q_st : kind[i] == 1 ? a.k_st : a.v_st;
+        const int64_t sh = kind[i] == 0 ? a.q_sh : kind[i] == 1 ? a.k_sh : a.v_sh;
+        step[i] = st * (int64_t)sizeof(T);
+        src[i] = kind[i] == 3 ? nullptr : static_cast<const unsigned char *>(p) + t0 * step[i] + (h * sh + lane * VEC) * (int64_t)sizeof(T);
+        dst[i] = kind[i] == 0   ? static_cast<T *>(a.q_out) + h * a.qo_sh
+                 : kind[i] == 1 ? static_cast<T *>(a.k_cache) + h * a.kc_sh
+                                : static_cast<T *>(a.v_cache) + h * a.vc_sh + lane * VEC;
+    }
     grid_dependency_wait();
 
-    const T *q = static_cast<const T *>(a.q) + t * a.q_st + c;
-    const T *k = static_cast<const T *>(a.k) + t * a.k_st + c;
-    const T *v = static_cast<const T *>(a.v) + t * a.v_st + c;
-    auto load = [&](int r) {
-        const T *p = r < a.Hq             ? q + (int64_t)r * a.q_sh
-                     : r < a.Hq + a.Hkv ? k + (int64_t)(r - a.Hq) * a.k_sh
-                                        : v + (int64_t)(r - a.Hq - a.Hkv) * a.v_sh;
-        return *reinterpret_cast<const uint4 *>(p);
+    int ahead = (int)(t1 - t0);  // tokens not yet fetched
+    uint32_t fs = 0;             // stage of the next one
+    auto fetch = [&]() {
+        if (ahead-- > 0) {
+            const uint32_t to = smem_addr(ring) + fs + tid * 16;
+#pragma unroll
+            for (int i = 0; i < kRopeUnroll; ++i)
+                if (kind[i] != 3) {
+                    cp_async_16(to + i * (kRopeThreads * 16), src[i]);
+                    src[i] += step[i];
+                }
+        }
+        cp_async_commit();
+        fs = fs == (kRopeStages - 1) * stage_bytes ? 0 : fs + stage_bytes;
     };
-    uint4 w[kRopeUnroll];
 #pragma unroll
-    for (int i = 0; i < kRopeUnroll; ++i)
-        if (grp + i * GROUPS < rows) w[i] = load(grp + i * GROUPS);
+    for (int n = 0; n < kRopeStages - 1; ++n) fetch();
 
-    if (tid < a.rot / 2) {
-        // the angle in turns, reduced to [-1/2, 1/2] in fp64
-        const double turns = (double)a.positions[t] * a.inv_freq[tid] * 0.15915494309189533577;
-        float sn, cs;
-        sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
-        s_cs[tid] = make_float2(cs, sn);
-    }
-    const int64_t slot = a.slots[t];
-    const bool kept = slot >= 0 && slot < a.num_slots;
-    const int64_t page = kept ? slot / a.page_size : 0, off = kept ? slot % a.page_size : 0;
-    T *qo = static_cast<T *>(a.q_out) + t * a.qo_st + c;
-    T *kc = static_cast<T *>(a.k_cache) + page * a.kc_sp + off * a.kc_sn + c;
-    T *vc = static_cast<T *>(a.v_cache) + page * a.vc_sp + off * a.vc_sn + c;
-    __syncthreads();
-
-    // this lane's factors: y[i] = x[i] * cs[i] + partner[i] * sn[i]
-    float cs[VEC], sn[VEC];
-    const int half = a.rot / 2;
-    const bool turned = c < a.rot;
-    const int src = NEIGHBOURS ? lane : (c < half ? lane + half / VEC : lane - half / VEC);
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        cs[i] = 1.f, sn[i] = 0.f;
-        if (turned) {
-            const float2 f = s_cs[NEIGHBOURS ? (c + i) / 2 : (c < half ? c + i : c + i - half)];
-            cs[i] = f.x;
-            sn[i] = (NEIGHBOURS ? (i & 1) == 0 : c < half) ? -f.y : f.y;
+    // where channel ch is held: its lane, and its place among the lane's VEC
+    auto held = [&](int ch, int &l, int &at) {
+        if (NEIGHBOURS || ch >= a.rot) {
+            const int u = NEIGHBOURS ? ch : ch - a.rot;
+            l = turning + u / VEC, at = u % VEC;
+        } else {
+            const int u = ch < half ? ch : ch - half;
+            l = u / CH, at = (ch < half ? 0 : CH) + u % CH;
         }
+    };
+    // the pair whose factors this thread forms, for every batch
+    const int pair = tid % (kD / 2);
+    const bool turns_it = pair < half;
+    const int c1 = NEIGHBOURS || !turns_it ? 2 * pair : pair;
+    const int c2 = NEIGHBOURS || !turns_it ? c1 + 1 : c1 + half;
+    int l1, p1, l2, p2;
+    held(c1, l1, p1);
+    held(c2, l2, p2);
+    float w1[2], w2[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const T *w = static_cast<const T *>(y ? a.wk : a.wq);
+        w1[y] = w ? Elem<T>::to_float(w[c1]) : 1.f, w2[y] = w ? Elem<T>::to_float(w[c2]) : 1.f;
     }
+    const double turns_per = turns_it ? a.inv_freq[pair] : 0.0;
 
-    for (int r0 = grp; r0 - grp < rows; r0 += GROUPS * kRopeUnroll) {
+    uint32_t stage = 0;
+    for (int64_t first = t0; first < t1; first += kRopeBatch) {
+        __syncthreads();  // the previous batch's factors have been read
+        {
+            const int k = tid / (kD / 2);  // kRopeBatch x 64 threads: one a pair of each token
+            const int64_t t = first + k;
+            if (t < t1) {
+                // the angle in turns, reduced to [-1/2, 1/2] in fp64
+                const double turns = (double)a.positions[t] * turns_per * 0.15915494309189533577;
+                float sn, cs;
+                sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
 #pragma unroll
-        for (int i = 0; i < kRopeUnroll; ++i) {
-            const int r = r0 + i * GROUPS;
-            // whole warps take part in the shuffles: rows past the last one carry zeros
-            const bool real = r < rows;
-            const bool is_v = r >= a.Hq + a.Hkv;
-            if (!__any_sync(0xffffffffu, real)) continue;
-            uint4 u = real ? w[i] : make_uint4(0, 0, 0, 0);
-            float x[VEC];
-            RopeVec<T>::unpack(u, x);
-            const T *wt = static_cast<const T *>(r < a.Hq ? a.wq : a.wk);
-            float ss = 0.f;
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) ss = fmaf(x[j], x[j], ss);
-#pragma unroll
-            for (int d = LANES / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-            if (!is_v && wt) {
-                const float inv = rsqrtf(ss * (1.f / kD) + a.eps);
-                float wv[VEC];
-                RopeVec<T>::unpack(*reinterpret_cast<const uint4 *>(wt + c), wv);
-#pragma unroll
-                for (int j = 0; j < VEC; ++j) x[j] = x[j] * inv * wv[j];
-            }
-            float y[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                const float p = NEIGHBOURS ? x[j ^ 1] : __shfl_sync(0xffffffffu, x[j], src, LANES);
-                y[j] = turned ? fmaf(x[j], cs[j], p * sn[j]) : x[j];
-            }
-            if (!real) continue;
-            if (is_v) {
-                if (kept) *reinterpret_cast<uint4 *>(vc + (int64_t)(r - a.Hq - a.Hkv) * a.vc_sh) = u;
-            } else if (r < a.Hq) {
-                *reinterpret_cast<uint4 *>(qo + (int64_t)r * a.qo_sh) = RopeVec<T>::pack(y);
-            } else if (kept) {
-                *reinterpret_cast<uint4 *>(kc + (int64_t)(r - a.Hq) * a.kc_sh) = RopeVec<T>::pack(y);
+                for (int y = 0; y < 2; ++y) {
+                    auto put = [&](int l, int at, float f) { reinterpret_cast<float *>(&s_f[k][y][at >> 2][l])[at & 3] = f; };
+                    put(l1, p1, cs * w1[y]), put(l1, VEC + p1, -sn * w2[y]);
+                    put(l2, p2, cs * w2[y]), put(l2, VEC + p2, sn * w1[y]);
+                }
+                if (pair == 0) {
+                    const int64_t slot = a.slots[t];
+                    const bool kept = slot >= 0 && slot < a.num_slots;
+                    int64_t page = 0, off = 0;
+                    if (kept) {
+                        if ((slot >> 32) == 0) page = (uint32_t)slot / (uint32_t)a.page_size;  // the short division
+                        else page = slot / a.page_size;
+                        off = slot - page * a.page_size;
+                    }
+                    s_off[k][0] = t * a.qo_st;
+                    s_off[k][1] = kept ? page * a.kc_sp + off * a.kc_sn : -1;
+                    s_off[k][2] = kept ? page * a.vc_sp + off * a.vc_sn : -1;
+                }
             }
         }
+        __syncthreads();
+        const int n = (int)min((int64_t)kRopeBatch, t1 - first);
+        for (int k = 0; k < n; ++k) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRopeStages - 2) : "memory");
+            __syncwarp();  // the warp's lanes share its rows
+            const unsigned char *held_rows = ring + stage + (uint32_t)grp * (kD * sizeof(T));
 #pragma unroll
-        for (int i = 0; i < kRopeUnroll; ++i) {
-            const int r = r0 + GROUPS * (kRopeUnroll + i);
-            if (r < rows) w[i] = load(r);
+            for (int i = 0; i < kRopeUnroll; ++i) {
+                if (row0 + i * GROUPS >= row1) break;
+                const unsigned char *row = held_rows + i * (kRopeThreads * 16);
+                if (kind[i] >= 2) {  // a value row: as it is
+                    if (kind[i] == 2 && s_off[k][2] >= 0)
+                        *reinterpret_cast<uint4 *>(dst[i] + s_off[k][2]) = *reinterpret_cast<const uint4 *>(row + lane * 16);
+                    continue;
+                }
+                uint64_t x[P], z[P];
+                RopeChunk<T>::unpack(*reinterpret_cast<const uint2 *>(row + a0 * sizeof(T)), x);
+                RopeChunk<T>::unpack(*reinterpret_cast<const uint2 *>(row + b0 * sizeof(T)), z);
+                float inv = 1.f;
+                if (kind[i] ? a.wk : a.wq) {
+                    uint64_t s2 = fma2(z[0], z[0], mul2(x[0], x[0]));
+#pragma unroll
+                    for (int j = 1; j < P; ++j) s2 = fma2(z[j], z[j], fma2(x[j], x[j], s2));
+                    float ss, ss1;
+                    unpack2(s2, ss, ss1);
+                    ss += ss1;
+                    // the lanes of this row (another row of the warp may be of another kind)
+                    const unsigned mask = LANES == 32 ? 0xffffffffu : 0xffffu << (tid & 16);
+#pragma unroll
+                    for (int d = LANES / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(mask, ss, d);
+                    inv = rsqrtf(ss * (1.f / kD) + a.eps);
+                }
+                const uint64_t inv2 = pack2(inv, inv);
+                float4 f4[VEC / 2];
+#pragma unroll
+                for (int j = 0; j < VEC / 2; ++j) f4[j] = s_f[k][kind[i]][j][lane];
+                const uint64_t *f = reinterpret_cast<const uint64_t *>(f4);  // cos w: P + P pairs, sin w': P + P
+#pragma unroll
+                for (int j = 0; j < P; ++j) {
+                    const uint64_t px = NEIGHBOURS ? swap2(x[j]) : z[j], pz = NEIGHBOURS ? swap2(z[j]) : x[j];
+                    const uint64_t y = fma2(px, f[2 * P + j], mul2(x[j], f[j]));
+                    z[j] = mul2(fma2(pz, f[3 * P + j], mul2(z[j], f[P + j])), inv2);
+                    x[j] = mul2(y, inv2);
+                }
+                const int64_t off = s_off[k][kind[i]];
+                if (off >= 0) {
+                    *reinterpret_cast<uint2 *>(dst[i] + off + a0) = RopeChunk<T>::pack(x);
+                    *reinterpret_cast<uint2 *>(dst[i] + off + b0) = RopeChunk<T>::pack(z);
+                }
+            }
+            __syncwarp();  // its rows have been read
+            fetch();       // into the stage of the token before
+            stage = stage == (kRopeStages - 1) * stage_bytes ? 0 : stage + stage_bytes;
         }
     }
+    cp_async_wait_all();
 }
 
 }  // namespace think
