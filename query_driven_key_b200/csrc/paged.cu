@@ -87,10 +87,10 @@ think_status_t launch_paged_simt(const PagedArgs &a, const PagedPlan &p, cudaStr
 think_status_t launch_paged_tc(const PagedArgs &a, const PagedPlan &p, cudaStream_t st)
 {
     // rows of one TMA load: the largest power of two that divides the page, at most a tile
-    const int chunk = std::min(kPtBN, a.page_size & -a.page_size);
+    const int chunk = std::min(kPtBN, a.page.d & -a.page.d);
     CUtensorMap mk, mv;
-    if (!make_map_4d(&mk, THINK_BF16, a.k, kD, a.page_size, a.Hkv, a.num_pages, a.k_sn, a.k_sh, a.k_sp, 64, chunk, true) ||
-        !make_map_4d(&mv, THINK_BF16, a.v, kD, a.page_size, a.Hkv, a.num_pages, a.v_sn, a.v_sh, a.v_sp, 64, chunk, true))
+    if (!make_map_4d(&mk, THINK_BF16, a.k, kD, a.page.d, a.Hkv, a.num_pages, a.k_sn, a.k_sh, a.k_sp, 64, chunk, true) ||
+        !make_map_4d(&mv, THINK_BF16, a.v, kD, a.page.d, a.Hkv, a.num_pages, a.v_sn, a.v_sh, a.v_sp, 64, chunk, true))
         return THINK_ERR_CUDA;
     if (!ensure_smem(reinterpret_cast<const void *>(&paged_tc_kernel), p.smem)) return THINK_ERR_CUDA;
     const think_status_t rc =
@@ -163,7 +163,7 @@ think_status_t think_extend_pages(const int32_t *new_lens, const int32_t *kv_len
     a.T = T;
     a.limit = (int64_t)max_blocks * page_size;
     a.B = B;
-    a.page_size = page_size;
+    a.page = Divisor(page_size);
     a.n_free = n_free;
     // one block for a decode step's few rows; up to a cluster of eight for prompts
     int blocks = 1;
@@ -264,8 +264,8 @@ think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const
     a.k_sp = num_pages > 1 ? k_cache_strides[0] : kD, a.k_sh = Hkv > 1 ? k_cache_strides[1] : kD, a.k_sn = k_cache_strides[2];
     a.v_sp = num_pages > 1 ? v_cache_strides[0] : kD, a.v_sh = Hkv > 1 ? v_cache_strides[1] : kD, a.v_sn = v_cache_strides[2];
     a.table_ld = table_ld;
-    a.B = B, a.T = (int)T, a.Hkv = Hkv, a.G = G;
-    a.page_size = page_size, a.num_pages = num_pages, a.limit = max_blocks * page_size, a.window = window;
+    a.B = B, a.T = (int)T, a.Hkv = Hkv, a.group = Divisor(G), a.page = Divisor(page_size);
+    a.num_pages = num_pages, a.limit = max_blocks * page_size, a.window = window;
     a.rows_cap = p.rows_cap, a.parts = p.parts, a.sides = p.sides;
     a.scale_log2 = scale * 1.44269504088896341f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -293,10 +293,10 @@ think_status_t think_gather_pages(const void *cache, const int64_t cache_strides
     if (dtype == THINK_BF16)
         return launch_pdl(gather_pages_kernel<__nv_bfloat16>, grid, dim3(kGatherThreads), 0, st,
                           static_cast<const __nv_bfloat16 *>(cache), cache_strides[0], cache_strides[1], cache_strides[2],
-                          num_pages, page_size, block_table, table_ld, max_blocks, kv_lens, Hkv, N,
+                          num_pages, Divisor(page_size), block_table, table_ld, max_blocks, kv_lens, Hkv, N,
                           static_cast<__nv_bfloat16 *>(out));
     return launch_pdl(gather_pages_kernel<float>, grid, dim3(kGatherThreads), 0, st, static_cast<const float *>(cache),
-                      cache_strides[0], cache_strides[1], cache_strides[2], num_pages, page_size, block_table, table_ld,
+                      cache_strides[0], cache_strides[1], cache_strides[2], num_pages, Divisor(page_size), block_table, table_ld,
                       max_blocks, kv_lens, Hkv, N, static_cast<float *>(out));
 }
 

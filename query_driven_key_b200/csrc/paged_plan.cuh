@@ -29,7 +29,8 @@ struct PagedArgs {
     int64_t q_st, q_sh, o_st, o_sh;
     int64_t k_sp, k_sh, k_sn, v_sp, v_sh, v_sn;
     int64_t table_ld;
-    int B, T, Hkv, G, page_size, num_pages, limit, window;
+    Divisor group, page;  // query heads a KV head, rows a page
+    int B, T, Hkv, num_pages, limit, window;
     int rows_cap;  // rows of a partial that may hold data
     int parts;     // blocks of the attention launch
     int sides;     // partials of a piece: 2 where two warpgroups work on it
@@ -60,9 +61,9 @@ struct TileRange {
 template <int R, int BN>
 __device__ __forceinline__ TileRange tile_range(const PagedArgs &a, const Request &s, int qt)
 {
-    const int rows = s.n * a.G;
+    const int rows = s.n * a.group.d;
     const int r0 = qt * R, r1 = min(r0 + R, rows) - 1;
-    const int p0 = s.kv - s.n + r0 / a.G, p1 = s.kv - s.n + r1 / a.G;  // first and last position
+    const int p0 = s.kv - s.n + a.group.quot(r0), p1 = s.kv - s.n + a.group.quot(r1);  // first and last position
     TileRange t;
     t.lo = a.window > 0 ? max(0, p0 - a.window + 1) : 0;
     t.hi = max(p1 + 1, 0);
@@ -79,20 +80,39 @@ __device__ __forceinline__ TileRange tile_range(const PagedArgs &a, const Reques
 template <int R>
 __device__ __forceinline__ int row_tiles(const PagedArgs &a, const Request &s)
 {
-    return (s.n * a.G + R - 1) / R;
+    return (s.n * a.group.d + R - 1) / R;
 }
 
-// Key tiles of one KV head of request b.
+// Key tiles of row tiles [0, nt) of one KV head of a request, every `step`-th from `first`.
 template <int R, int BN>
-__device__ __forceinline__ int64_t head_units(const PagedArgs &a, const Request &s)
+__device__ __forceinline__ int64_t head_units(const PagedArgs &a, const Request &s, int first, int step)
 {
     const int nt = row_tiles<R>(a, s);
     int64_t u = 0;
-    for (int qt = 0; qt < nt; ++qt) {
+    for (int qt = first; qt < nt; qt += step) {
         const TileRange t = tile_range<R, BN>(a, s, qt);
         u += t.j1 - t.j0;
     }
     return u;
+}
+
+template <typename T>
+__device__ __forceinline__ T warp_sum(T x)
+{
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+    return x;
+}
+template <typename T>
+__device__ __forceinline__ T warp_scan(T x)  // inclusive
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    return x;
 }
 
 // A place in the sequence of key tiles.
@@ -106,41 +126,76 @@ struct PlanSmem {
     Place place;
 };
 
-// The total number of key tiles and the place of tile *first (a function of
-// the total); all NT threads call it.  Thread t keeps request t's share where
-// B <= NT, so that the lengths are read once.
+// The total number of key tiles and the place of tile first(total); all NT
+// threads call it.  Up to NT / 32 requests: a warp each, a lane a row tile (a
+// prompt has hundreds of row tiles); more: a thread each.
 template <int R, int BN, int NT, typename First>
 __device__ __forceinline__ int64_t plan(const PagedArgs &a, PlanSmem *sm, First first)
 {
     static_assert(NT % 32 == 0 && NT <= 1024, "whole warps");
+    constexpr int W = NT / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int64_t mine = 0, sum = 0;
+    if (a.B <= W) {
+        Request s;
+        int64_t uh = 0;  // of one head of the warp's request
+        if (warp < a.B) {
+            s = load_request(a, warp);
+            uh = warp_sum(head_units<R, BN>(a, s, lane, 32));
+        }
+        if (lane == 0) sm->ws[warp] = uh * a.Hkv;
+        __syncthreads();
+        int64_t total = 0, before = 0;
+        for (int w = 0; w < W; ++w) {
+            if (w == warp) before = total;
+            total += sm->ws[w];
+        }
+        int64_t rem = first(total) - before;
+        if (rem >= 0 && rem < uh * a.Hkv) {  // this warp's request holds the place
+            Place p;
+            p.b = warp;
+            p.h = (int)(rem / uh);
+            rem -= p.h * uh;
+            const int nt = row_tiles<R>(a, s);
+            for (int q0 = 0; q0 < nt; q0 += 32) {
+                int n = 0;
+                if (q0 + lane < nt) {
+                    const TileRange t = tile_range<R, BN>(a, s, q0 + lane);
+                    n = t.j1 - t.j0;
+                }
+                const int end = warp_scan(n);
+                if (rem >= end - n && rem < end) {
+                    p.qt = q0 + lane;
+                    p.off = (int)rem - (end - n);
+                    sm->place = p;
+                }
+                rem -= __shfl_sync(0xffffffffu, end, 31);
+                if (rem < 0) break;
+            }
+        }
+        __syncthreads();
+        return total;
+    }
+    int64_t mine = 0, sum = 0;  // the last request of this thread, all of them
     for (int b = tid; b < a.B; b += NT) {
-        mine = head_units<R, BN>(a, load_request(a, b)) * a.Hkv;
+        mine = head_units<R, BN>(a, load_request(a, b), 0, 1) * a.Hkv;
         sum += mine;
     }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    sum = warp_sum(sum);
     if (lane == 0) sm->ws[warp] = sum;
     __syncthreads();
     int64_t total = 0;
-    for (int w = 0; w < NT / 32; ++w) total += sm->ws[w];
+    for (int w = 0; w < W; ++w) total += sm->ws[w];
     __syncthreads();
     const int64_t u = first(total);
     int64_t base = 0;
     for (int b0 = 0; b0 < a.B && base <= u; b0 += NT) {
         const int b = b0 + tid;
-        const int64_t x0 = a.B <= NT ? mine : (b < a.B ? head_units<R, BN>(a, load_request(a, b)) * a.Hkv : 0);
-        int64_t x = x0;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += y;
-        }
+        const int64_t x0 = a.B <= NT ? mine : (b < a.B ? head_units<R, BN>(a, load_request(a, b), 0, 1) * a.Hkv : 0);
+        int64_t x = warp_scan(x0);
         if (lane == 31) sm->ws[warp] = x;
         __syncthreads();
         int64_t chunk = 0;
-        for (int w = 0; w < NT / 32; ++w) {
+        for (int w = 0; w < W; ++w) {
             if (w == warp) x += chunk;
             chunk += sm->ws[w];
         }
@@ -252,18 +307,24 @@ __device__ __forceinline__ void store_out4<__nv_bfloat16>(__nv_bfloat16 *p, floa
 }
 
 // Join the pieces of the item that the border between parts c - 1 and c cuts,
-// if that is the first border inside the item (blockIdx.x = c - 1; blockIdx.y
-// and the warps share the rows).  In order of the parts, so that the result
-// does not depend on timing:
+// if that is the first border inside the item (blockIdx.x = c - 1; the blocks
+// of one x share the rows):
 //     m = max m_i,  l = sum l_i 2^(m_i - m),  out = sum O_i 2^(m_i - m) / l.
-// A row that sees no key has l = 0 and gets zeros.
+// A row that sees no key has l = 0 and gets zeros.  With fewer rows than warps
+// several warps share a row's partials (a decode step has few rows and up to
+// hundreds of partials each); the lanes of a warp read 32 (m, l) at once, and
+// the loads of the O_i do not wait for one another.  The order of the sums is
+// fixed, so that the result does not depend on timing.
 constexpr int kMergeThreads = 256;
 constexpr int kMergeSlices = 8;
 
 template <typename T, int R, int BN, bool TWO_SIDES>
 __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedArgs a)
 {
+    constexpr int W = kMergeThreads / 32;
     __shared__ PlanSmem sm;
+    __shared__ __align__(16) float s_o[W][kD];
+    __shared__ float2 s_ml[W];
     const int c = (int)blockIdx.x + 1;
     const int64_t total = plan<R, BN, kMergeThreads>(a, &sm, [&](int64_t n) { return part_begin(n, c, a.parts); });
     const int64_t u = part_begin(total, c, a.parts);
@@ -274,34 +335,75 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
     if (p.off == 0 || part_begin(total, c - 1, a.parts) > start) return;
     const Request s = load_request(a, p.b);
     const TileRange t = tile_range<R, BN>(a, s, p.qt);
+    // the last part that holds a piece of the item: that of its last key tile
     const int64_t end = start + (t.j1 - t.j0);
-    int last = c;  // the last part that holds a piece of the item
-    while (part_begin(total, last + 1, a.parts) < end) ++last;
-    const int rows = min(R, s.n * a.G - p.qt * R);
-    const int lane = threadIdx.x & 31;
+    int lo = c, hi = a.parts - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (part_begin(total, mid, a.parts) < end) lo = mid;
+        else hi = mid - 1;
+    }
+    const int rows = min(R, s.n * a.group.d - p.qt * R);
     const bool two_sides = TWO_SIDES && rows <= R / 2;  // the two sides hold the same rows
-    for (int r = (int)blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5); r < rows;
-         r += kMergeSlices * (kMergeThreads / 32)) {
+    const int count = (lo - c + 2) * (two_sides ? 2 : 1);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // rows blockIdx.y, blockIdx.y + kMergeSlices, ..., `share` warps a row
+    const int mine = (rows - (int)blockIdx.y + kMergeSlices - 1) / kMergeSlices;
+    const int share = mine >= W ? 1 : mine > 4 ? 1 : mine > 2 ? 2 : mine > 1 ? 4 : W;
+    for (int k0 = 0; k0 < mine; k0 += W / share) {
+        const int k = k0 + warp / share, r = (int)blockIdx.y + k * kMergeSlices;
+        const bool real = k < mine;
         const int side0 = TWO_SIDES && !two_sides ? r / (R / 2) : 0;
         const int row = TWO_SIDES && !two_sides ? r % (R / 2) : r;
+        auto partial = [&](int i) {
+            const int part = c - 1 + (two_sides ? i >> 1 : i);
+            return part_at(a, part, part == c - 1 ? 1 : 0, two_sides ? i & 1 : side0) + (int64_t)row * kPartLd;
+        };
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = c - 1; i <= last; ++i)
-            for (int side = side0; side <= (two_sides ? 1 : side0); ++side) {
-                const float *x = part_at(a, i, i == c - 1 ? 1 : 0, side) + (int64_t)row * kPartLd;
-                const float mi = __ldcg(x + kD), li = __ldcg(x + kD + 1);
-                const float2 a0 = __ldcg(reinterpret_cast<const float2 *>(x) + 2 * lane);
-                const float2 a1 = __ldcg(reinterpret_cast<const float2 *>(x) + 2 * lane + 1);
-                const float mn = fmaxf(m, mi), ref = mn == -INFINITY ? 0.f : mn;
-                const float f = exp2f(m - ref), g = exp2f(mi - ref);
-                o.x = o.x * f + a0.x * g, o.y = o.y * f + a0.y * g;
-                o.z = o.z * f + a1.x * g, o.w = o.w * f + a1.y * g;
-                l = l * f + li * g;
+        if (real)
+            for (int i0 = warp % share; i0 < count; i0 += 32 * share) {  // partials i0, i0 + share, ...
+                const int n = min(32, (count - i0 + share - 1) / share);
+                float2 ml = make_float2(-INFINITY, 0.f);
+                if (lane < n) ml = __ldcg(reinterpret_cast<const float2 *>(partial(i0 + lane * share) + kD));
+                float mn = ml.x;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
+                mn = fmaxf(mn, m);
+                const float ref = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2f(m - ref), g = exp2f(ml.x - ref);
+                l = l * f + warp_sum(ml.y * g);
+                m = mn;
+                o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll 8
+                for (int i = 0; i < n; ++i) {
+                    const float *x = partial(i0 + i * share);
+                    const float2 a0 = __ldcg(reinterpret_cast<const float2 *>(x) + 2 * lane);
+                    const float2 a1 = __ldcg(reinterpret_cast<const float2 *>(x) + 2 * lane + 1);
+                    const float gi = __shfl_sync(0xffffffffu, g, i);
+                    o.x += a0.x * gi, o.y += a0.y * gi, o.z += a1.x * gi, o.w += a1.y * gi;
+                }
+            }
+        if (share > 1) {  // the row's first warp adds the others' sums in order
+            __syncthreads();
+            *reinterpret_cast<float4 *>(&s_o[warp][4 * lane]) = o;
+            if (lane == 0) s_ml[warp] = make_float2(m, l);
+            __syncthreads();
+            if (warp % share) continue;
+            for (int w = warp + 1; w < warp + share; ++w) {
+                const float2 y = s_ml[w];
+                const float4 q = *reinterpret_cast<const float4 *>(&s_o[w][4 * lane]);
+                const float mn = fmaxf(m, y.x), ref = mn == -INFINITY ? 0.f : mn;
+                const float f = exp2f(m - ref), g = exp2f(y.x - ref);
+                o.x = o.x * f + q.x * g, o.y = o.y * f + q.y * g, o.z = o.z * f + q.z * g, o.w = o.w * f + q.w * g;
+                l = l * f + y.y * g;
                 m = mn;
             }
+        }
+        if (!real) continue;
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        const int gr = p.qt * R + r, tok = gr / a.G, g = gr % a.G;
-        store_out4(static_cast<T *>(a.out) + (int64_t)(s.row0 + tok) * a.o_st + (int64_t)(p.h * a.G + g) * a.o_sh + 4 * lane,
+        const int gr = p.qt * R + r, tok = a.group.quot(gr), g = gr - tok * a.group.d;
+        store_out4(static_cast<T *>(a.out) + (int64_t)(s.row0 + tok) * a.o_st + (int64_t)(p.h * a.group.d + g) * a.o_sh + 4 * lane,
                    make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     }
 }

@@ -36,7 +36,7 @@ template <int R>
 __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedArgs a)
 {
     constexpr int BN = kSimtBN, MI = R / 16;
-    extern __shared__ float smem[];
+    extern __shared__ __align__(16) float smem[];
     float *qs = smem, *ks = qs + R * kD, *vs = ks + BN * kD, *ps = vs + BN * kD;  // ps: [BN][R]
     __shared__ PlanSmem sm;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -48,15 +48,15 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedArg
     const int64_t u0 = part_begin(total, part, a.parts), u1 = part_begin(total, part + 1, a.parts);
     if (u0 >= u1) return;
     for (Walk<R, BN> w(a, sm.place, u1 - u0); w.live(); w.next()) {
-        const int rows = min(R, w.s.n * a.G - w.p.qt * R);
+        const int rows = min(R, w.s.n * a.group.d - w.p.qt * R);
         __syncthreads();  // the previous item's tiles have been read
         for (int i = tid; i < R * 32; i += kSimtThreads) {
             const int r = i >> 5, c4 = i & 31;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (r < rows) {
-                const int gr = w.p.qt * R + r;
-                x = load_row4(static_cast<const float *>(a.q) + (int64_t)(w.s.row0 + gr / a.G) * a.q_st +
-                              (int64_t)(w.p.h * a.G + gr % a.G) * a.q_sh + 4 * c4);
+                const int gr = w.p.qt * R + r, tok = a.group.quot(gr), g = gr - tok * a.group.d;
+                x = load_row4(static_cast<const float *>(a.q) + (int64_t)(w.s.row0 + tok) * a.q_st +
+                              (int64_t)(w.p.h * a.group.d + g) * a.q_sh + 4 * c4);
             }
             *reinterpret_cast<float4 *>(qs + r * kD + 4 * c4) = x;
         }
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedArg
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             const int r = ty + 16 * i;
-            pos[i] = r < rows ? w.s.kv - w.s.n + (w.p.qt * R + r) / a.G : -1;
+            pos[i] = r < rows ? w.s.kv - w.s.n + a.group.quot(w.p.qt * R + r) : -1;
             m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[i][j] = 0.f;
@@ -76,10 +76,10 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedArg
                 const int n = i >> 5, c4 = i & 31, key = jt * BN + n;
                 float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
                 if (key >= w.t.lo && key < w.t.hi) {
-                    const int j = key / a.page_size;
+                    const int j = a.page.quot(key);
                     const int page = a.table[(int64_t)w.p.b * a.table_ld + j];
                     if ((unsigned)page < (unsigned)a.num_pages) {
-                        const int64_t off = key - (int64_t)j * a.page_size;
+                        const int64_t off = key - (int64_t)j * a.page.d;
                         x = load_row4(static_cast<const float *>(a.k) + page * a.k_sp + w.p.h * a.k_sh + off * a.k_sn + 4 * c4);
                         y = load_row4(static_cast<const float *>(a.v) + page * a.v_sp + w.p.h * a.v_sh + off * a.v_sn + 4 * c4);
                     } else if (c4 == 0) {
@@ -156,9 +156,9 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedArg
             if (r >= rows) continue;
             if (w.whole) {
                 const float inv = s > 0.f ? 1.f / s : 0.f;
-                const int gr = w.p.qt * R + r;
-                float *dst = static_cast<float *>(a.out) + (int64_t)(w.s.row0 + gr / a.G) * a.o_st +
-                         (int64_t)(w.p.h * a.G + gr % a.G) * a.o_sh + 4 * tx;
+                const int gr = w.p.qt * R + r, tok = a.group.quot(gr), g = gr - tok * a.group.d;
+                float *dst = static_cast<float *>(a.out) + (int64_t)(w.s.row0 + tok) * a.o_st +
+                             (int64_t)(w.p.h * a.group.d + g) * a.o_sh + 4 * tx;
                 store_out4(dst, make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv));
                 store_out4(dst + 64, make_float4(o[i][4] * inv, o[i][5] * inv, o[i][6] * inv, o[i][7] * inv));
             } else {

@@ -26,8 +26,8 @@
 // Value rows behind the request's last token are set to zero in shared memory
 // before their product, whatever the page holds there.
 //
-// Warps: 8 softmax, 1 producer (a lane a load), 1 for the products (which owns
-// the TMEM), 2 idle.  TMEM columns: S_t (and P_t in its first half) at 128 t, O_t at
+// Warps: 8 softmax, 1 producer (a lane a load), 2 for the products (a warpgroup
+// each; the first owns the TMEM), 1 idle.  TMEM columns: S_t (and P_t in its first half) at 128 t, O_t at
 // 256 + 128 t.  Every wait is bounded; one that runs out sets the status bit and
 // the block's abort flag, after which every wait returns at once and all warps
 // still reach the final barrier, where the TMEM is released.
@@ -41,20 +41,72 @@ namespace think {
 
 constexpr int kPtRows = 256;
 constexpr int kPtBN = 128;
-constexpr int kPtThreads = 384;  // 12 warps: the last two only lend their registers
+constexpr int kPtThreads = 384;  // 12 warps: the last one only lends its registers
 constexpr int kPtProducer = 8;
 constexpr int kPtMma = 9;
 constexpr int kPtStages = 5;
 constexpr uint32_t kPtTile = 32768u;
 constexpr float kPtLazy = 8.f;
+constexpr int kPtEarly = 96;  // keys of a tile whose P is handed over while the rest's is formed
 
 struct PtBars {
-    uint64_t full[kPtStages], empty[kPtStages], q_full[2], s_full[2], p_full[2], o_full[2], done;
+    // A wait tells only a phase's parity, so that who waits on a barrier has to
+    // see each of its phases: what both warpgroups' products use (rows split)
+    // has barriers of its own, and so has what one of them uses (keys split).
+    uint64_t full[3][kPtStages];  // loads: for both, for warpgroup 0, for 1
+    uint64_t empty[kPtStages];
+    uint64_t q_full[3];  // Q of warpgroup 0, of 1, of a split item
+    uint64_t s_full[2], o_full[2];
+    uint64_t p_full[4];  // [t]: the early part of P, [2 + t]: all of it
+    uint64_t turn[2];    // warpgroup t's products may go next
+    uint64_t done;
     uint32_t tmem;
     uint32_t abort_flag;
 };
 
 constexpr size_t paged_tc_smem() { return 1024u + (2u + kPtStages) * (size_t)kPtTile; }
+
+// A warp's bounded wait.  The phase has mostly completed already: one try and
+// one vote; the block's abort flag is looked at only while it has not.
+__device__ __forceinline__ bool pt_wait(uint32_t bar, uint32_t parity, volatile uint32_t *abort_flag, unsigned *status,
+                                        unsigned code)
+{
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_flag, status, code));
+}
+
+// A value that every lane holds, in a form that the compiler knows to be the
+// same in all of them: the products' operands then stay in uniform registers
+// (otherwise each of the 16 tcgen05.mma of a tile took about 80 cycles to
+// issue, more than the 64 that it runs).
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
+// 16 bytes from global memory, zeros if not `real`.  (A volatile statement: as
+// a plain load the compiler moves each one down to its use, and a row tile's 16
+// loads then wait one after another, 14000 cycles instead of 2000.)
+__device__ __forceinline__ uint4 load16(const void *p, bool real)
+{
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(p), "r"((uint32_t)real));
+    return v;
+}
 
 // One item's shape for the block's roles.
 struct PtItem {
@@ -65,7 +117,7 @@ struct PtItem {
 __device__ __forceinline__ PtItem pt_item(const PagedArgs &a, const Walk<kPtRows, kPtBN> &w)
 {
     PtItem x;
-    x.rows = min(kPtRows, w.s.n * a.G - w.p.qt * kPtRows);
+    x.rows = min(kPtRows, w.s.n * a.group.d - w.p.qt * kPtRows);
     x.split = x.rows <= 128;
     x.n = w.j1 - w.j0;
     return x;
@@ -93,6 +145,17 @@ struct PtOrder {
         value = true;
         return i - pairs;
     }
+    // the places of key tile j and of value tile j among them
+    __device__ __forceinline__ int key(int j) const
+    {
+        const int first = min(ahead, n);
+        return j < first ? j : 2 * j - first + 1;
+    }
+    __device__ __forceinline__ int value(int j) const
+    {
+        const int first = min(ahead, n), pairs = n - first;
+        return j < pairs ? first + 2 * j : first + pairs + j;
+    }
 };
 
 __global__ void __launch_bounds__(kPtThreads, 1)
@@ -109,16 +172,20 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile uint32_t *abort_flag = &bars.abort_flag;
     const uint32_t full0 = smem_addr(bars.full), empty0 = smem_addr(bars.empty), qfull0 = smem_addr(bars.q_full),
-                   sfull0 = smem_addr(bars.s_full), pfull0 = smem_addr(bars.p_full), ofull0 = smem_addr(bars.o_full), done = smem_addr(&bars.done);
+                   sfull0 = smem_addr(bars.s_full), pfull0 = smem_addr(bars.p_full), ofull0 = smem_addr(bars.o_full), turn0 = smem_addr(bars.turn), done = smem_addr(&bars.done);
     if (tid == 0) {
-        for (int s = 0; s < kPtStages; ++s) mbar_init(full0 + 8 * s, 1), mbar_init(empty0 + 8 * s, 1);
+        for (int s = 0; s < 3 * kPtStages; ++s) mbar_init(full0 + 8 * s, 1);
+        for (int s = 0; s < kPtStages; ++s) mbar_init(empty0 + 8 * s, 2);
+        mbar_init(qfull0 + 16, 8);
         for (int t = 0; t < 2; ++t) {
             mbar_init(qfull0 + 8 * t, 4);
             mbar_init(sfull0 + 8 * t, 1);
             mbar_init(pfull0 + 8 * t, 4);
+            mbar_init(pfull0 + 16 + 8 * t, 4);
             mbar_init(ofull0 + 8 * t, 1);
+            mbar_init(turn0 + 8 * t, 1);
         }
-        mbar_init(done, 1);
+        mbar_init(done, 2);
         bars.abort_flag = 0;
         fence_barrier_init();
         prefetch_tensormap(&tm_k);
@@ -141,14 +208,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const Place place = plan_sm.place;
 
     // A softmax thread holds a row of 128 logits: 384 x 168 registers at launch
-    // = 256 x 208 for the softmax warps + 128 x 88 for the others.
+    // = 256 x 216 for the softmax warps + 128 x 72 for the others.
     if (warp >= 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kPtProducer) {
         // ---------------------------------------------------------- producer
         const int per_tile = kPtBN / chunk;  // loads of one 64-channel half
         const uint32_t bytes = (uint32_t)chunk * 128u;
         uint32_t ld = 0;                     // loads issued: stage ld % kPtStages
+        uint32_t phases = 0, used = 0;       // of each full barrier its next phase; of each stage the last one's set
         bool ok = true;
         for (W w(a, place, units); w.live() && ok; w.next()) {
             const PtItem x = pt_item(a, w);
@@ -156,25 +224,28 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             // this lane's rows of load i: the table entry (-1: no key of them is
             // seen; read an iteration ahead, looked at when it is used) and the
             // row in the page
-            auto locate = [&](int i, int &entry, int &row, bool &needed, bool &value) {
-                const int key = (w.j0 + order.tile(i, value)) * kPtBN + (lane >> 1) * chunk;
+            auto locate = [&](int i, int &entry, int &row, bool &needed, bool &value, int &tile) {
+                tile = order.tile(i, value);
+                const int key = (w.j0 + tile) * kPtBN + (lane >> 1) * chunk;
                 needed = (lane >> 1) < per_tile && key < w.t.hi && key + chunk > w.t.lo;
-                const int j = key / a.page_size;
-                row = key - j * a.page_size;
+                const int j = a.page.quot(key);
+                row = key - j * a.page.d;
                 entry = needed ? a.table[(int64_t)w.p.b * a.table_ld + j] : -1;
             };
-            int entry, row;
+            int entry, row, tile;
             bool needed, value;
-            locate(0, entry, row, needed, value);
+            locate(0, entry, row, needed, value, tile);
             for (int i = 0; i < order.loads(); ++i, ++ld) {
-                const int cur_entry = entry, cur_row = row;
+                const int cur_entry = entry, cur_row = row, cur_tile = tile;
                 const bool cur_needed = needed, cur_value = value;
-                if (i + 1 < order.loads()) locate(i + 1, entry, row, needed, value);
-                const uint32_t s = ld % kPtStages, full = full0 + 8 * s;
+                if (i + 1 < order.loads()) locate(i + 1, entry, row, needed, value, tile);
+                const uint32_t s = ld % kPtStages;
                 if (ld >= kPtStages)
-                    ok = tc_wait(empty0 + 8 * s, ((ld / kPtStages) - 1) & 1, abort_flag, a.status, THINK_DEVICE_TIMEOUT_EMPTY);
-                ok = __all_sync(0xffffffffu, ok);
+                    ok = pt_wait(empty0 + 8 * s, ((ld / kPtStages) - 1) & 1, abort_flag, a.status, THINK_DEVICE_TIMEOUT_EMPTY);
                 if (!ok) break;
+                const uint32_t set = x.split ? 1u + (cur_tile & 1) : 0u, full = full0 + 8 * (set * kPtStages + s);
+                phases ^= 1u << (set * kPtStages + s);
+                used = (used & ~(3u << (2 * s))) | set << (2 * s);
                 if (lane == 0) mbar_arrive_expect_tx(full, kPtTile);
                 __syncwarp();
                 if ((lane >> 1) < per_tile) {
@@ -187,119 +258,124 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
         }
         if (!ok)  // the loads in flight land before the block ends
-            for (uint32_t i = ld > kPtStages ? ld - kPtStages : 0; i < ld; ++i)
-                mbar_wait_bounded(full0 + 8 * (i % kPtStages), (i / kPtStages) & 1, a.status, THINK_DEVICE_TIMEOUT_FULL);
+            for (uint32_t s = 0; s < min(ld, (uint32_t)kPtStages); ++s) {
+                const uint32_t b = (used >> (2 * s) & 3u) * kPtStages + s;
+                mbar_wait_bounded(full0 + 8 * b, (phases >> b & 1u) ^ 1u, a.status, THINK_DEVICE_TIMEOUT_FULL);
+            }
         __syncwarp();
-    } else if (warp == kPtMma) {
+    } else if (warp == kPtMma || warp == kPtMma + 1) {
         // ------------------------------------------------------ the products
+        // One warp a softmax warpgroup t: what it issues waits for one thing
+        // after another (keys, values, P), and the other warp's products run
+        // meanwhile.  The two take turns, a tile's product with V and the next
+        // one's logits at a time: otherwise their products would mix on the
+        // tensor core and both warpgroups form their P at the same time, with
+        // the tensor core idle.
         constexpr uint32_t idesc_s = tc05::idesc_bf16_f32<128, 128, false>();
         constexpr uint32_t idesc_o = tc05::idesc_bf16_f32_bmn<128, 128>();
-        uint32_t ld = 0;              // loads taken
-        uint32_t items = 0, np0 = 0, np1 = 0;  // items begun, P tiles taken
+        const int t = warp - kPtMma;
+        const bool leader = elect_one();
+        uint32_t base = 0;              // loads of the items before
+        uint32_t nq = 0, nqs = 0, np = 0, nt = t ^ 1;  // items begun (rows split, keys split), P tiles taken, turns
+        uint32_t phases = 0;               // of each full barrier of the two sets waited on
         bool ok = true;
         auto wait = [&](uint32_t bar, uint32_t phase, unsigned code) {
-            if (ok) ok = __all_sync(0xffffffffu, tc_wait(bar, phase & 1, abort_flag, a.status, code));
+            if (ok) ok = pt_wait(bar, phase & 1, abort_flag, a.status, code);
         };
-        auto stage = [&](uint32_t i) { return smem_addr(ring + (i % kPtStages) * kPtTile); };
-        auto take = [&](uint32_t i) { wait(full0 + 8 * (i % kPtStages), i / kPtStages, THINK_DEVICE_TIMEOUT_FULL); };
-        auto release = [&](uint32_t i) {
-            if (lane == 0 && ok) tc05::commit(empty0 + 8 * (i % kPtStages));
-        };
-        auto logits = [&](int t, int qt, uint32_t i) {  // S_t = Q_qt K^T
-            if (!ok) return;
-            tc05::fence_after_sync();
-            if (lane == 0) {
-                const uint32_t qa = smem_addr(qs + qt * kPtTile), kb = stage(i);
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint32_t o = (uint32_t)(ks >> 2) * 16384u + (uint32_t)(ks & 3) * 32u;
-                    tc05::mma_bf16(tmem + 128u * t, tc05::smem_desc(qa + o, 16u, 1024u, tc05::kLayoutSwizzle128B),
-                                   tc05::smem_desc(kb + o, 16u, 1024u, tc05::kLayoutSwizzle128B), idesc_s, ks > 0);
-                }
-                tc05::commit(sfull0 + 8 * t);
-            }
-        };
-        auto values = [&](int t, uint32_t i, bool accumulate) {  // O_t (+)= P_t V
-            wait(pfull0 + 8 * t, t ? np1++ : np0++, THINK_DEVICE_TIMEOUT_FULL);
-            if (!ok) return;
-            tc05::fence_after_sync();
-            if (lane == 0) {
-                const uint32_t vb = stage(i);
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    tc05::mma_bf16_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * ks,
-                                      tc05::smem_desc(vb + 2048u * ks, 16384u, 1024u, tc05::kLayoutSwizzle128B), idesc_o,
-                                      accumulate || ks > 0);
-            }
-        };
-        // value rows from the request's end on are zeroed before their product
-        auto clean = [&](uint32_t i, int jt, int kv) {
-            const int from = max(0, kv - jt * kPtBN);
-            if (!ok || from >= kPtBN) return;
-            unsigned char *v = ring + (i % kPtStages) * kPtTile;
-            for (int j = lane; j < (kPtBN - from) * 8; j += 32) {
-                *reinterpret_cast<uint4 *>(v + from * 128 + j * 16) = make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(v + 16384 + from * 128 + j * 16) = make_uint4(0, 0, 0, 0);
-            }
-            tc05::fence_proxy_async_smem();
-            __syncwarp();
-        };
-        for (W w(a, place, units); w.live() && ok; w.next(), ++items) {
+        const uint64_t q_desc = tc05::smem_desc(smem_addr(qs), 16u, 1024u, tc05::kLayoutSwizzle128B);
+        const uint64_t k_desc = tc05::smem_desc(smem_addr(ring), 16u, 1024u, tc05::kLayoutSwizzle128B);
+        const uint64_t v_desc = tc05::smem_desc(smem_addr(ring), 16384u, 1024u, tc05::kLayoutSwizzle128B);
+        const uint32_t s_tmem = uniform(tmem + 128u * t), o_tmem = s_tmem + 256u;
+        const uint32_t s_bar = uniform(sfull0 + 8 * t), o_bar = uniform(ofull0 + 8 * t);
+        for (W w(a, place, units); w.live() && ok; w.next()) {
             const PtItem x = pt_item(a, w);
-            wait(qfull0, items, THINK_DEVICE_TIMEOUT_FULL);
-            if (!x.split) {
-                take(ld);
-                logits(0, 0, ld);
-                wait(qfull0 + 8, items, THINK_DEVICE_TIMEOUT_FULL);
-                logits(1, 1, ld);
-                release(ld++);
-                for (int j = 0; j < x.n && ok; ++j) {
-                    const uint32_t vi = ld++, ki = ld;
-                    const bool more = j + 1 < x.n;
-                    take(vi);
-                    clean(vi, w.j0 + j, w.s.kv);
-                    values(0, vi, j > 0);
-                    if (more) {
-                        take(ki);
-                        logits(0, 0, ki);
-                    } else if (lane == 0 && ok) {
-                        tc05::commit(ofull0);
-                    }
-                    values(1, vi, j > 0);
-                    release(vi);
-                    if (more) {
-                        logits(1, 1, ki);
-                        release(ki);
-                        ++ld;
-                    } else if (lane == 0 && ok) {
-                        tc05::commit(ofull0 + 8);
-                    }
+            const PtOrder order{x.split ? 2 : 1, x.n};
+            const int j0 = x.split ? t : 0, step = x.split ? 2 : 1;
+            // a key or value tile is released by both warps, or twice by the one that uses it
+            auto release = [&](uint32_t s) {
+                if (leader && ok) {
+                    tc05::commit(empty0 + 8 * s);
+                    if (x.split) tc05::commit(empty0 + 8 * s);
                 }
-            } else {
-                wait(qfull0 + 8, items, THINK_DEVICE_TIMEOUT_FULL);
-                for (int j = 0; j < min(2, x.n); ++j) {
-                    take(ld);
-                    logits(j, 0, ld);
-                    release(ld++);
-                }
-                for (int j = 0; j < x.n && ok; ++j) {
-                    const int t = j & 1;
-                    take(ld);
-                    clean(ld, w.j0 + j, w.s.kv);
-                    values(t, ld, j > 1);
-                    release(ld++);
-                    if (j + 2 < x.n) {
-                        take(ld);
-                        logits(t, 0, ld);
-                        release(ld++);
-                    } else if (lane == 0 && ok) {
-                        tc05::commit(ofull0 + 8 * t);
+            };
+            // load i of the item has arrived: its stage
+            auto take = [&](int i) {
+                const uint32_t s = (base + i) % kPtStages, set = x.split ? 1u + t : 0u;
+                const uint32_t bit = (x.split ? kPtStages : 0) + s;
+                wait(full0 + 8 * (set * kPtStages + s), phases >> bit, THINK_DEVICE_TIMEOUT_FULL);
+                phases ^= 1u << bit;
+                return s;
+            };
+            auto logits = [&](uint32_t s) {  // S = Q K^T, K in stage s
+                if (!ok) return;
+                const uint64_t qd = q_desc + uniform(x.split ? 0u : (uint32_t)t * (kPtTile >> 4));
+                const uint64_t kd = k_desc + uniform(s * (kPtTile >> 4));
+                if (leader) {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const uint32_t o = ((uint32_t)(ks >> 2) * 16384u + (uint32_t)(ks & 3) * 32u) >> 4;
+                        tc05::mma_bf16(s_tmem, qd + o, kd + o, idesc_s, ks > 0);
                     }
+                    tc05::commit(s_bar);
                 }
+                release(s);
+            };
+            auto pass = [&]() {
+                if (leader) mbar_arrive(turn0 + 8 * (t ^ 1));
+            };
+            if (x.split) wait(qfull0 + 16, nqs++, THINK_DEVICE_TIMEOUT_FULL);
+            else wait(qfull0 + 8 * t, nq++, THINK_DEVICE_TIMEOUT_FULL);
+            if (j0 < x.n) {
+                const uint32_t s = take(order.key(j0));
+                tc05::fence_after_sync();
+                logits(s);
             }
+            for (int j = j0; j < x.n && ok; j += step) {  // O (+)= P V_j, then the next tile's logits
+                const uint32_t s = take(order.value(j));
+                if (!ok) break;
+                // value rows from the request's end on are zeroed before the product
+                const int from = max(0, w.s.kv - (w.j0 + j) * kPtBN);
+                if (from < kPtBN) {
+                    unsigned char *v = ring + s * kPtTile;
+                    for (int c = lane; c < (kPtBN - from) * 8; c += 32) {
+                        *reinterpret_cast<uint4 *>(v + from * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(v + 16384 + from * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                    tc05::fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                const bool next = j + step < x.n;
+                const uint32_t sk = next ? take(order.key(j + step)) : 0;
+                const uint64_t vd = v_desc + uniform(s * (kPtTile >> 4));
+                const bool more = uniform(j > j0) != 0;
+                auto issue = [&](int k0, int k1) {
+                    if (!ok) return;
+                    tc05::fence_after_sync();
+                    if (leader) {
+#pragma unroll
+                        for (int ks = k0; ks < k1; ++ks)
+                            tc05::mma_bf16_ts(o_tmem, s_tmem + 8u * ks, vd + 128u * ks, idesc_o, ks > 0 || more);
+                    }
+                };
+                wait(turn0 + 8 * t, nt++, THINK_DEVICE_TIMEOUT_FULL);
+                wait(pfull0 + 8 * t, np, THINK_DEVICE_TIMEOUT_FULL);
+                issue(0, kPtEarly / 16);
+                wait(pfull0 + 16 + 8 * t, np, THINK_DEVICE_TIMEOUT_FULL);
+                issue(kPtEarly / 16, kPtBN / 16);
+                ++np;
+                if (next) logits(sk);
+                else if (leader && ok) tc05::commit(o_bar);
+                pass();
+                release(s);
+            }
+            if (x.split && t == 1 && (x.n & 1)) {  // the turn of a tile that there is not
+                wait(turn0 + 8, nt++, THINK_DEVICE_TIMEOUT_FULL);
+                pass();
+            }
+            base += order.loads();
         }
         // no product and no arrival may be under way when the block ends
-        if (lane == 0) {
+        if (leader) {
             tc05::commit(done);
             mbar_wait_bounded(done, 0, a.status, THINK_DEVICE_TIMEOUT_FULL);
         }
@@ -307,7 +383,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     }
     } else {
         // ----------------------------------------------------------- softmax
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int t = warp >> 2, wq = warp & 3;
         const int r = 32 * wq + lane;  // this thread's row of the tile
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * wq) << 16);
@@ -318,8 +394,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         uint32_t ns = 0, no = 0;
         bool was_split = false;
         auto wait = [&](uint32_t bar, uint32_t phase) {
-            tc_wait(bar, phase & 1, abort_flag, a.status, THINK_DEVICE_TIMEOUT_FULL);
-            __syncwarp();
+            pt_wait(bar, phase & 1, abort_flag, a.status, THINK_DEVICE_TIMEOUT_FULL);
         };
         // Q of an item: a warpgroup's own rows, the products of whose last tile
         // have been waited for; in and around split items the rows are shared,
@@ -331,21 +406,26 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const int first = x.split ? 64 * t : 0, count = x.split ? 64 : 128;
             unsigned char *dst = qs + (x.split ? 0u : (uint32_t)t * kPtTile);
             const int c16 = tid & 15;
-            for (int i = first + ((tid & 127) >> 4); i < first + count; i += 8) {
-                const int local = x.split ? i : 128 * t + i;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (local < x.rows) {
-                    const int gr = w.p.qt * kPtRows + local;
-                    v = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) +
-                                                              (int64_t)(w.s.row0 + gr / a.G) * a.q_st +
-                                                              (int64_t)(w.p.h * a.G + gr % a.G) * a.q_sh + 8 * c16));
-                    v.x ^= flip, v.y ^= flip, v.z ^= flip, v.w ^= flip;
+            for (int i0 = first + ((tid & 127) >> 4); i0 < first + count; i0 += 64) {
+                uint4 v[8];  // loads first: one latency for eight rows
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int local = i0 + 8 * k + (x.split ? 0 : 128 * t);
+                    const int gr = w.p.qt * kPtRows + local, tok = a.group.quot(gr), g = gr - tok * a.group.d;
+                    v[k] = load16(static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)(w.s.row0 + tok) * a.q_st +
+                                      (int64_t)(w.p.h * a.group.d + g) * a.q_sh + 8 * c16,
+                                  local < x.rows);
                 }
-                *reinterpret_cast<uint4 *>(dst + (c16 >> 3) * 16384 + i * 128 + (((c16 & 7) ^ (i & 7)) << 4)) = v;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int i = i0 + 8 * k;
+                    v[k].x ^= flip, v[k].y ^= flip, v[k].z ^= flip, v[k].w ^= flip;
+                    *reinterpret_cast<uint4 *>(dst + (c16 >> 3) * 16384 + i * 128 + (((c16 & 7) ^ (i & 7)) << 4)) = v[k];
+                }
             }
             tc05::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(qfull0 + 8 * t);
+            if (lane == 0) mbar_arrive(qfull0 + (x.split ? 16 : 8 * t));
         };
         W w(a, place, units);
         if (w.live()) load_q(w);
@@ -355,7 +435,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const int row = w.p.qt * kPtRows + (x.split ? r : 128 * t + r);
             const bool real = row - w.p.qt * kPtRows < x.rows;
             const bool warp_real = __any_sync(0xffffffffu, real);
-            const int pos = real ? base + row / a.G : -1;
+            // (a row that is not real takes part as the last one of its request: what it holds is not stored)
+            const int tok = a.group.quot(row);
+            const int pos = base + (real ? tok : w.s.n - 1);
             float m = -INFINITY, l = 0.f;
             const int step = x.split ? 2 : 1, j0 = x.split ? t : 0;
             for (int j = j0; j < x.n; j += step) {
@@ -376,9 +458,16 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         for (int c = 0; c < kPtBN; ++c)
                             if (c >= chi || c < clo) u[c >> 5][c & 31] = 0xff800000u;  // -inf
                     }
-                    float mx = __uint_as_float(u[0][0]);
+                    float mx4[4];
 #pragma unroll
-                    for (int c = 1; c < kPtBN; ++c) mx = fmaxf(mx, __uint_as_float(u[c >> 5][c & 31]));
+                    for (int i = 0; i < 4; ++i) {
+                        mx4[i] = __uint_as_float(u[i][0]);
+#pragma unroll
+                        for (int c = 1; c < 31; c += 2)
+                            mx4[i] = fmaxf(fmaxf(mx4[i], __uint_as_float(u[i][c])), __uint_as_float(u[i][c + 1]));
+                        mx4[i] = fmaxf(mx4[i], __uint_as_float(u[i][31]));
+                    }
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
                     const bool grow = (mx - m) * sl > kPtLazy;  // NaN (both -inf): false
                     if (__any_sync(0xffffffffu, grow)) {
                         const float f = grow ? exp2_approx((m - mx) * sl) : 1.f;
@@ -415,15 +504,23 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                             p[c] = *reinterpret_cast<const uint32_t *>(&b);
                         }
                         tc05::tmem_st16(s_addr + 16u * i, p);
+                        if (i == kPtEarly / 32 - 1) {
+                            tc05::tmem_st_wait();
+                            tc05::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(pfull0 + 8 * t);
+                        }
                     }
                     float s0, s1;
                     unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
                     l += s0 + s1;
                     tc05::tmem_st_wait();
                     tc05::fence_before_sync();
+                } else if (lane == 0) {
+                    mbar_arrive(pfull0 + 8 * t);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(pfull0 + 8 * t);
+                if (lane == 0) mbar_arrive(pfull0 + 16 + 8 * t);
             }
             const bool any = j0 < x.n;  // this warpgroup had key tiles
             const bool join = x.split && w.whole && x.n > 1;
@@ -443,8 +540,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     for (int c = 0; c < 32; ++c) o[c] = 0u;
                 }
             };
-            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + (int64_t)(w.s.row0 + row / a.G) * a.o_st +
-                                 (int64_t)(w.p.h * a.G + row % a.G) * a.o_sh;
+            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + (int64_t)(w.s.row0 + tok) * a.o_st +
+                                 (int64_t)(w.p.h * a.group.d + row - tok * a.group.d) * a.o_sh;
             auto store_o = [&](int i, const float (&o)[32], float f) {
 #pragma unroll
                 for (int c = 0; c < 32; c += 8)

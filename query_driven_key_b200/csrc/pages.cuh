@@ -16,6 +16,21 @@ constexpr int kPagesThreads = 1024;
 constexpr int kPagesMaxCluster = 8;
 constexpr int kMaxPosition = 1 << 30;  // positions and lengths stay below, so that tile arithmetic fits 32 bits
 
+// Quotients by a divisor that a launch fixes, of dividends in [0, 2^31): the
+// high word of a product with a reciprocal of 33 bits (Granlund and Montgomery,
+// "Division by invariant integers using multiplication").
+struct Divisor {
+    int d, shift;
+    uint32_t mul;
+    Divisor() = default;
+    explicit Divisor(int divisor) : d(divisor), shift(0)
+    {
+        while ((1ll << shift) < d) ++shift;
+        mul = (uint32_t)((((1ull << shift) - (uint64_t)d) << 32) / (uint64_t)d + 1);
+    }
+    __device__ __forceinline__ int quot(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+};
+
 struct ExtendArgs {
     const int32_t *new_lens, *free_pages, *free_count;
     const int32_t *kv_lens;
@@ -23,7 +38,8 @@ struct ExtendArgs {
     int64_t *slots;
     unsigned *status;
     int64_t table_ld, T, limit;  // limit: the tokens that a table row can hold
-    int B, page_size, n_free;
+    Divisor page;
+    int B, n_free;
 };
 
 // Inclusive scan of one value a thread over the block (kPagesThreads
@@ -84,7 +100,7 @@ __global__ void __launch_bounds__(kPagesThreads) extend_pages_kernel(const Exten
         const int64_t row_end = rows + block_scan_i64(n, ws, &total);
         // a request whose tokens do not fit its table row or the row arrays takes no page
         const bool fits = (int64_t)len + n <= a.limit && row_end <= a.T;
-        const int need = fits ? (int)(((int64_t)len + n + a.page_size - 1) / a.page_size - ((int64_t)len + a.page_size - 1) / a.page_size) : 0;
+        const int need = fits ? a.page.quot(len + n + a.page.d - 1) - a.page.quot(len + a.page.d - 1) : 0;
         const int64_t page_end = pages + block_scan_i64(need, ws, &taken);
         const bool admitted = fits && (need == 0 || page_end <= count);
         s_row[tid] = row_end - n;
@@ -115,16 +131,16 @@ __global__ void __launch_bounds__(kPagesThreads) extend_pages_kernel(const Exten
             const int pos = len0 + (int)(r - s_row[l]);
             int64_t slot = -1;
             if (s_free[l] >= 0) {
-                const int j = pos / a.page_size, before = (len0 + a.page_size - 1) / a.page_size;
+                const int j = a.page.quot(pos), before = a.page.quot(len0 + a.page.d - 1);
                 int64_t at = (int64_t)(b0 + l) * a.table_ld + j;
                 int page;
                 if (j < before) {
                     page = a.table[at];
                 } else {
                     page = a.free_pages[count - 1 - (s_free[l] + (j - before))];
-                    if (pos - j * a.page_size == 0) a.table[at] = page;
+                    if (pos - j * a.page.d == 0) a.table[at] = page;
                 }
-                if (page >= 0) slot = (int64_t)page * a.page_size + (pos - j * a.page_size);
+                if (page >= 0) slot = (int64_t)page * a.page.d + (pos - j * a.page.d);
                 else bits |= THINK_DEVICE_BAD_PAGE;
             }
             a.positions[r] = pos;
@@ -153,7 +169,7 @@ constexpr int kGatherRows = 4;
 
 template <typename TIn>
 __global__ void __launch_bounds__(kGatherThreads)
-    gather_pages_kernel(const TIn *__restrict__ cache, int64_t sp, int64_t sh, int64_t sn, int num_pages, int page_size,
+    gather_pages_kernel(const TIn *__restrict__ cache, int64_t sp, int64_t sh, int64_t sn, int num_pages, Divisor page_size,
                         const int32_t *__restrict__ table, int64_t table_ld, int max_blocks,
                         const int32_t *__restrict__ kv_lens, int Hkv, int64_t N, TIn *__restrict__ out)
 {
@@ -163,7 +179,7 @@ __global__ void __launch_bounds__(kGatherThreads)
     grid_dependency_wait();
     const int head = blockIdx.y, b = head / Hkv, h = head % Hkv;
     const int c = (threadIdx.x % LANES) * VEC;
-    const int64_t len = min((int64_t)max(kv_lens[b], 0), (int64_t)max_blocks * page_size);
+    const int64_t len = min((int64_t)max(kv_lens[b], 0), (int64_t)max_blocks * page_size.d);
     const int64_t n0 = (int64_t)blockIdx.x * (STEP * kGatherRows) + threadIdx.x / LANES;
     uint4 v[kGatherRows];
 #pragma unroll
@@ -171,11 +187,11 @@ __global__ void __launch_bounds__(kGatherThreads)
         const int64_t n = n0 + i * STEP;
         v[i] = make_uint4(0, 0, 0, 0);
         if (n < len && n < N) {
-            const int j = (int)n / page_size;
+            const int j = page_size.quot((int)n);
             const int page = table[(int64_t)b * table_ld + j];
             if ((unsigned)page < (unsigned)num_pages)
                 v[i] = *reinterpret_cast<const uint4 *>(cache + (int64_t)page * sp + (int64_t)h * sh +
-                                                        (int64_t)((int)n - j * page_size) * sn + c);
+                                                        (int64_t)((int)n - j * page_size.d) * sn + c);
         }
     }
 #pragma unroll

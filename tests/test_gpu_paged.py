@@ -209,7 +209,11 @@ SHAPES = [
     ([64, 0, 1, 33, 0, 2], [10, 50, 400, 0, 0, 127], 8, 2, 32, 0), ([5, 70], [30, 0], 7, 1, 16, 0),
     ([40], [90], 12, 1, 256, 0), ([20, 1], [600, 900], 16, 2, 48, 0),
     ([1, 200, 1], [900, 100, 30], 8, 2, 16, 64), ([300], [0], 4, 2, 32, 100), ([2, 40], [400, 300], 4, 1, 64, 1),
-    ([1, 1], [3000, 10], 8, 1, 16, 500), ([150], [500], 3, 1, 48, 333), ([600], [200], 2, 2, 112, 0)]
+    ([1, 1], [3000, 10], 8, 1, 16, 500), ([150], [500], 3, 1, 48, 333), ([600], [200], 2, 2, 112, 0),
+    # many key tiles a block: one request's keys shared by all blocks, rows shared, several items a block, both kinds in turn
+    ([1], [150000], 4, 1, 64, 0), ([3], [120000], 8, 1, 16, 90001), ([200], [40000], 2, 1, 128, 0),
+    ([1] * 40, [37 * i for i in range(40)], 16, 8, 16, 0), ([1, 300, 2, 70, 1, 140] * 4, [900, 10, 3000, 200, 0, 1500] * 4, 8, 4, 32, 0),
+    ([2, 260, 1, 33] * 6, [1400, 0, 700, 2100] * 6, 12, 4, 48, 600)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
