@@ -3,12 +3,12 @@
 //
 // Query rows: row r of request b is its new token r / G and query head r % G of
 // the KV head's group, so that the G heads that share keys fill a tile
-// together.  An item is (request, KV head, tile of R rows); its work is the
-// number of BN-key tiles that any of its rows sees (at least 1, so that rows
-// that see nothing are still written).  The items' key tiles form one sequence,
-// requests first, then heads, then row tiles; block i of P takes the i-th of P
-// equal parts of it.  Whatever the mix of lengths, all blocks get the same work
-// to within one key tile; an item that a part's border cuts is computed in
+// together.  An item is (request, KV head, tile of R rows); its work, in units,
+// is the number of BN-key tiles that any of its rows sees (at least 1, so that
+// rows that see nothing are still written) and a fixed cost.  The items' units
+// form one sequence, requests first, then heads, then row tiles; block i of P
+// takes the i-th of P equal parts of it.  Whatever the mix of lengths, all blocks
+// get the same work to within a unit; an item that a part's border cuts is computed in
 // pieces, each piece leaves its (max, sum, O) in the workspace, and
 // merge_kernel joins them in order.  Lengths stay on the device: the plan is
 // recomputed from q_start and kv_lens by every launch, so that a captured
@@ -77,13 +77,18 @@ __device__ __forceinline__ TileRange tile_range(const PagedArgs &a, const Reques
     return t;
 }
 
+// What an item costs beyond its key tiles (its queries, its output, the
+// pipeline's start and end), in key tiles: the sequence that is divided counts
+// it before the item's first tile.
+constexpr int kItemCost = 2;
+
 template <int R>
 __device__ __forceinline__ int row_tiles(const PagedArgs &a, const Request &s)
 {
     return (s.n * a.group.d + R - 1) / R;
 }
 
-// Key tiles of row tiles [0, nt) of one KV head of a request, every `step`-th from `first`.
+// Units of one KV head of a request: the key tiles and costs of its row tiles, every `step`-th from `first`.
 template <int R, int BN>
 __device__ __forceinline__ int64_t head_units(const PagedArgs &a, const Request &s, int first, int step)
 {
@@ -91,7 +96,7 @@ __device__ __forceinline__ int64_t head_units(const PagedArgs &a, const Request 
     int64_t u = 0;
     for (int qt = first; qt < nt; qt += step) {
         const TileRange t = tile_range<R, BN>(a, s, qt);
-        u += t.j1 - t.j0;
+        u += kItemCost + t.j1 - t.j0;
     }
     return u;
 }
@@ -115,9 +120,9 @@ __device__ __forceinline__ T warp_scan(T x)  // inclusive
     return x;
 }
 
-// A place in the sequence of key tiles.
+// A place in the sequence.
 struct Place {
-    int b, h, qt, off;  // the item, and the key tiles of it that lie before the place
+    int b, h, qt, off;  // the item, and the units of it that lie before the place
 };
 
 // Scratch of plan(): one block's.
@@ -126,7 +131,7 @@ struct PlanSmem {
     Place place;
 };
 
-// The total number of key tiles and the place of tile first(total); all NT
+// The total number of units and the place of unit first(total); all NT
 // threads call it.  Up to NT / 32 requests: a warp each, a lane a row tile (a
 // prompt has hundreds of row tiles); more: a thread each.
 template <int R, int BN, int NT, typename First>
@@ -160,7 +165,7 @@ __device__ __forceinline__ int64_t plan(const PagedArgs &a, PlanSmem *sm, First 
                 int n = 0;
                 if (q0 + lane < nt) {
                     const TileRange t = tile_range<R, BN>(a, s, q0 + lane);
-                    n = t.j1 - t.j0;
+                    n = kItemCost + t.j1 - t.j0;
                 }
                 const int end = warp_scan(n);
                 if (rem >= end - n && rem < end) {
@@ -210,8 +215,8 @@ __device__ __forceinline__ int64_t plan(const PagedArgs &a, PlanSmem *sm, First 
             rem -= p.h * uh;
             for (p.qt = 0;; ++p.qt) {
                 const TileRange t = tile_range<R, BN>(a, s, p.qt);
-                if (rem < t.j1 - t.j0) break;
-                rem -= t.j1 - t.j0;
+                if (rem < kItemCost + t.j1 - t.j0) break;
+                rem -= kItemCost + t.j1 - t.j0;
             }
             p.off = (int)rem;
             sm->place = p;
@@ -222,7 +227,7 @@ __device__ __forceinline__ int64_t plan(const PagedArgs &a, PlanSmem *sm, First 
     return total;
 }
 
-// First key tile of part `part` of the min(parts, total) parts, none of which
+// First unit of part `part` of the min(parts, total) parts, none of which
 // is empty; total for the parts behind the last one.
 __device__ __forceinline__ int64_t part_begin(int64_t total, int part, int parts)
 {
@@ -237,7 +242,7 @@ struct Walk {
     const PagedArgs &a;
     Place p;
     Request s;
-    int64_t left;   // key tiles of the part from this item on
+    int64_t left;   // units of the part from the place on
     TileRange t;    // the item
     int j0, j1;     // the piece
     bool whole, head;  // head: the piece begins with the item
@@ -251,10 +256,11 @@ struct Walk {
     __device__ __forceinline__ void set()
     {
         t = tile_range<R, BN>(a, s, p.qt);
-        j0 = t.j0 + p.off;
-        j1 = (int)min((int64_t)t.j1, j0 + left);
-        head = p.off == 0;
+        j0 = t.j0 + max(0, p.off - kItemCost);
+        j1 = (int)min((int64_t)t.j1, t.j0 + max((int64_t)0, p.off - kItemCost + left));
+        head = j0 == t.j0;
         whole = head && j1 == t.j1;
+        if (j0 == j1) left = 0;  // the part ends before the item's first tile
     }
     __device__ __forceinline__ bool live() const { return left > 0; }
     __device__ __forceinline__ void assign(const Walk &o)
@@ -263,14 +269,14 @@ struct Walk {
     }
     __device__ __forceinline__ void next()
     {
-        left -= j1 - j0;
+        left -= kItemCost + t.j1 - t.j0 - p.off;
         if (left <= 0) return;
         p.off = 0;
         if (++p.qt == row_tiles<R>(a, s)) {
             p.qt = 0;
             if (++p.h == a.Hkv) {
                 p.h = 0;
-                do {  // the sequence has `left` more tiles: a request with rows follows
+                do {  // the sequence has `left` more units: a request with rows follows
                     if (++p.b == a.B) {
                         left = 0;
                         return;
@@ -331,8 +337,8 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedA
     grid_dependency_wait();  // every block waits, so that this grid ends after the attention
     if (u >= total) return;
     const Place p = sm.place;
-    const int64_t start = u - p.off;  // the item's first key tile in the sequence
-    if (p.off == 0 || part_begin(total, c - 1, a.parts) > start) return;
+    const int64_t start = u - p.off + kItemCost;  // the item's first key tile in the sequence
+    if (u <= start || part_begin(total, c - 1, a.parts) > start) return;
     const Request s = load_request(a, p.b);
     const TileRange t = tile_range<R, BN>(a, s, p.qt);
     // the last part that holds a piece of the item: that of its last key tile

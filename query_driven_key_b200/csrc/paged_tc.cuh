@@ -92,6 +92,27 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// The largest of a row's 128 logits.
+__device__ __forceinline__ float row_max(const uint32_t (&u)[4][32])
+{
+    float m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = __uint_as_float(u[i][0]);
+#pragma unroll
+        for (int c = 1; c < 31; c += 2) m[i] = max3(m[i], __uint_as_float(u[i][c]), __uint_as_float(u[i][c + 1]));
+        m[i] = fmaxf(m[i], __uint_as_float(u[i][31]));
+    }
+    return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+
 // 16 bytes from global memory, zeros if not `real`.  (A volatile statement: as
 // a plain load the compiler moves each one down to its use, and a row tile's 16
 // loads then wait one after another, 14000 cycles instead of 2000.)
@@ -406,22 +427,22 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const int first = x.split ? 64 * t : 0, count = x.split ? 64 : 128;
             unsigned char *dst = qs + (x.split ? 0u : (uint32_t)t * kPtTile);
             const int c16 = tid & 15;
-            for (int i0 = first + ((tid & 127) >> 4); i0 < first + count; i0 += 64) {
-                uint4 v[8];  // loads first: one latency for eight rows
+            const int i0 = first + ((tid & 127) >> 4);
+            uint4 v[16];  // loads first: one latency for all rows
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int local = i0 + 8 * k + (x.split ? 0 : 128 * t);
-                    const int gr = w.p.qt * kPtRows + local, tok = a.group.quot(gr), g = gr - tok * a.group.d;
-                    v[k] = load16(static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)(w.s.row0 + tok) * a.q_st +
-                                      (int64_t)(w.p.h * a.group.d + g) * a.q_sh + 8 * c16,
-                                  local < x.rows);
-                }
+            for (int k = 0; k < 16; ++k) {
+                const int local = i0 + 8 * k + (x.split ? 0 : 128 * t);
+                const int gr = w.p.qt * kPtRows + local, tok = a.group.quot(gr), g = gr - tok * a.group.d;
+                v[k] = load16(static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)(w.s.row0 + tok) * a.q_st +
+                                  (int64_t)(w.p.h * a.group.d + g) * a.q_sh + 8 * c16,
+                              local < x.rows && 8 * k < count);
+            }
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int i = i0 + 8 * k;
-                    v[k].x ^= flip, v[k].y ^= flip, v[k].z ^= flip, v[k].w ^= flip;
+            for (int k = 0; k < 16; ++k) {
+                const int i = i0 + 8 * k;
+                v[k].x ^= flip, v[k].y ^= flip, v[k].z ^= flip, v[k].w ^= flip;
+                if (8 * k < count)
                     *reinterpret_cast<uint4 *>(dst + (c16 >> 3) * 16384 + i * 128 + (((c16 & 7) ^ (i & 7)) << 4)) = v[k];
-                }
             }
             tc05::fence_proxy_async_smem();
             __syncwarp();
@@ -458,18 +479,37 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         for (int c = 0; c < kPtBN; ++c)
                             if (c >= chi || c < clo) u[c >> 5][c & 31] = 0xff800000u;  // -inf
                     }
-                    float mx4[4];
+                    // The weights are formed with the reference as it stands,
+                    // beside the search for the maximum; where that has grown
+                    // too much (a few times an item), they are formed again.
+                    if (j == j0) m = row_max(u);
+                    uint64_t sum[4];
+                    uint64_t nm2;
+                    auto weights = [&](int i) {  // P of the keys 32 i .. (its columns of S have been read)
+                        uint32_t p[16];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        mx4[i] = __uint_as_float(u[i][0]);
+                        for (int c = 0; c < 16; ++c) {
+                            const uint64_t z =
+                                fma2(pack2(__uint_as_float(u[i][2 * c]), __uint_as_float(u[i][2 * c + 1])), sl2, nm2);
+                            float p0, p1;
+                            unpack2(z, p0, p1);
+                            p0 = exp2_approx(p0), p1 = exp2_approx(p1);
+                            sum[c & 3] = add2(sum[c & 3], pack2(p0, p1));
+                            p[c] = bf16_pair(p0, p1);
+                        }
+                        tc05::tmem_st16(s_addr + 16u * i, p);
+                    };
+                    const float mx = row_max(u);
+#pragma unroll 1
+                    for (;;) {
+                        const float nm = m == -INFINITY ? 0.f : -m * sl;
+                        nm2 = pack2(nm, nm);
 #pragma unroll
-                        for (int c = 1; c < 31; c += 2)
-                            mx4[i] = fmaxf(fmaxf(mx4[i], __uint_as_float(u[i][c])), __uint_as_float(u[i][c + 1]));
-                        mx4[i] = fmaxf(mx4[i], __uint_as_float(u[i][31]));
-                    }
-                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-                    const bool grow = (mx - m) * sl > kPtLazy;  // NaN (both -inf): false
-                    if (__any_sync(0xffffffffu, grow)) {
+                        for (int i = 0; i < 4; ++i) sum[i] = 0;
+#pragma unroll
+                        for (int i = 0; i < kPtEarly / 32; ++i) weights(i);
+                        const bool grow = (mx - m) * sl > kPtLazy;  // NaN (both -inf): false
+                        if (!__any_sync(0xffffffffu, grow)) break;
                         const float f = grow ? exp2_approx((m - mx) * sl) : 1.f;
                         if (grow) m = mx;
                         l *= f;
@@ -485,42 +525,23 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                             }
                         }
                     }
-                    const float nm = m == -INFINITY ? 0.f : -m * sl;
-                    const uint64_t nm2 = pack2(nm, nm);
-                    uint64_t sum[4] = {0, 0, 0, 0};
+                    tc05::tmem_st_wait();
+                    tc05::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pfull0 + 8 * t);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            const int k = 32 * i + 2 * c;
-                            const uint64_t z = fma2(pack2(__uint_as_float(u[k >> 5][k & 31]),
-                                                          __uint_as_float(u[k >> 5][(k & 31) + 1])), sl2, nm2);
-                            float z0, z1;
-                            unpack2(z, z0, z1);
-                            const float p0 = exp2_approx(z0), p1 = exp2_approx(z1);
-                            sum[c & 3] = add2(sum[c & 3], pack2(p0, p1));
-                            const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-                            p[c] = *reinterpret_cast<const uint32_t *>(&b);
-                        }
-                        tc05::tmem_st16(s_addr + 16u * i, p);
-                        if (i == kPtEarly / 32 - 1) {
-                            tc05::tmem_st_wait();
-                            tc05::fence_before_sync();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(pfull0 + 8 * t);
-                        }
-                    }
+                    for (int i = kPtEarly / 32; i < 4; ++i) weights(i);
+                    tc05::tmem_st_wait();
+                    tc05::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(pfull0 + 16 + 8 * t);
                     float s0, s1;
                     unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), s0, s1);
                     l += s0 + s1;
-                    tc05::tmem_st_wait();
-                    tc05::fence_before_sync();
                 } else if (lane == 0) {
                     mbar_arrive(pfull0 + 8 * t);
+                    mbar_arrive(pfull0 + 16 + 8 * t);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(pfull0 + 16 + 8 * t);
             }
             const bool any = j0 < x.n;  // this warpgroup had key tiles
             const bool join = x.split && w.whole && x.n > 1;
