@@ -454,8 +454,8 @@ think_status_t think_norm_rope_append(const void *q, const int64_t q_strides[2],
                                       const int64_t q_out_strides[2], void *k_cache, const int64_t k_cache_strides[3],
                                       void *v_cache, const int64_t v_cache_strides[3], int num_pages, int page_size,
                                       void *stream);
-/* think_paged_attn: causal attention of the new tokens over the pages; two
- * launches.  The i-th new token of request b, of n_b = q_start[b+1] -
+/* think_paged_attn: causal attention of the new tokens over the pages; one
+ * launch.  The i-th new token of request b, of n_b = q_start[b+1] -
  * q_start[b], has position p = kv_lens[b] - n_b + i (kv_lens counts the new
  * tokens, whose keys are in the pages already) and sees the keys j <= p, with
  * window > 0 only those with j > p - window:
@@ -472,10 +472,12 @@ think_status_t think_norm_rope_append(const void *q, const int64_t q_strides[2],
  * last token), may be anything, their table entries too.  A needed page outside
  * the pool counts as zero keys and values, with THINK_DEVICE_BAD_PAGE in the
  * status word.
- *   workspace: think_paged_attn_workspace_size() bytes (it depends on T * G
- * only up to 128 rows, and on nothing else), 16-byte aligned, zeroed once
- * before its first use (the status word; the rest is scratch).  Results do not
- * depend on timing.  Any Hq that is a multiple of Hkv (G <= 4096). */
+ *   workspace: think_paged_attn_workspace_size() bytes (they depend on dtype
+ * and, up to 128 rows, on T * G), 16-byte aligned, zeroed once before its first
+ * use: it begins with the status word and counters that every call leaves at
+ * zero, at the same place whatever the shape, so that one workspace serves calls
+ * of any shape it is large enough for, captured ones too; use it for this call
+ * alone.  Results do not depend on timing.  Any Hq that is a multiple of Hkv (G <= 4096). */
 size_t think_paged_attn_workspace_size(int64_t T, int Hq, int Hkv, int d, think_dtype_t dtype);
 think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const void *k_cache,
                                 const int64_t k_cache_strides[3], const void *v_cache, const int64_t v_cache_strides[3],

@@ -20,6 +20,7 @@ namespace think {
 namespace {
 
 constexpr size_t kPagedHeader = 256;     // status word + reserved, start of a workspace
+constexpr size_t kPagedTickets = 2048;   // then the attention's counters
 constexpr int kPageStep = 16;            // page sizes are multiples of 16 rows
 constexpr int64_t kExtendRowsPerBlock = 4096;
 
@@ -70,7 +71,8 @@ PagedPlan plan_paged(think_dtype_t dtype, int64_t T, int G, int max_new)
     }
     // (the same for 16 and 64 rows, so that max_new does not change the workspace)
     p.rows_cap = (int)std::min<int64_t>(dtype == THINK_BF16 ? 128 : 64, T * G);
-    p.ws_bytes = kPagedHeader + sizeof(float) * (size_t)p.parts * 2 * p.sides * (size_t)p.rows_cap * kPartLd;
+    static_assert(kPagedTickets >= 2 * kTargetSMs * sizeof(unsigned), "a counter a part");
+    p.ws_bytes = kPagedHeader + kPagedTickets + sizeof(float) * (size_t)p.parts * 2 * p.sides * (size_t)p.rows_cap * kPartLd;
     return p;
 }
 
@@ -78,10 +80,7 @@ template <int R>
 think_status_t launch_paged_simt(const PagedArgs &a, const PagedPlan &p, cudaStream_t st)
 {
     if (!ensure_smem(reinterpret_cast<const void *>(&paged_simt_kernel<R>), p.smem)) return THINK_ERR_CUDA;
-    const think_status_t rc = launch_pdl(paged_simt_kernel<R>, dim3((unsigned)p.parts), dim3(kSimtThreads), p.smem, st, a);
-    if (rc != THINK_OK) return rc;
-    return launch_pdl(paged_merge_kernel<float, R, kSimtBN, false>, dim3((unsigned)(p.parts - 1), kMergeSlices),
-                      dim3(kMergeThreads), 0, st, a);
+    return launch_pdl(paged_simt_kernel<R>, dim3((unsigned)p.parts), dim3(kSimtThreads), p.smem, st, a);
 }
 
 think_status_t launch_paged_tc(const PagedArgs &a, const PagedPlan &p, cudaStream_t st)
@@ -93,11 +92,7 @@ think_status_t launch_paged_tc(const PagedArgs &a, const PagedPlan &p, cudaStrea
         !make_map_4d(&mv, THINK_BF16, a.v, kD, a.page.d, a.Hkv, a.num_pages, a.v_sn, a.v_sh, a.v_sp, 64, chunk, true))
         return THINK_ERR_CUDA;
     if (!ensure_smem(reinterpret_cast<const void *>(&paged_tc_kernel), p.smem)) return THINK_ERR_CUDA;
-    const think_status_t rc =
-        launch_pdl(paged_tc_kernel, dim3((unsigned)p.parts), dim3(kPtThreads), p.smem, st, mk, mv, a, chunk);
-    if (rc != THINK_OK) return rc;
-    return launch_pdl(paged_merge_kernel<__nv_bfloat16, kPtRows, kPtBN, true>, dim3((unsigned)(p.parts - 1), kMergeSlices),
-                      dim3(kMergeThreads), 0, st, a);
+    return launch_pdl(paged_tc_kernel, dim3((unsigned)p.parts), dim3(kPtThreads), p.smem, st, mk, mv, a, chunk);
 }
 
 template <typename T, bool NEIGHBOURS>
@@ -258,7 +253,8 @@ think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const
     a.q = q, a.k = k_cache, a.v = v_cache, a.out = out;
     a.q_start = q_start, a.kv_lens = kv_lens, a.table = block_table;
     a.status = static_cast<unsigned *>(workspace);
-    a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + kPagedHeader);
+    a.part = reinterpret_cast<float *>(static_cast<unsigned char *>(workspace) + kPagedHeader + kPagedTickets);
+    a.tickets = reinterpret_cast<unsigned *>(static_cast<unsigned char *>(workspace) + kPagedHeader);
     a.q_st = q_strides[0], a.q_sh = q_strides[1], a.o_st = out_strides[0], a.o_sh = out_strides[1];
     // the stride of a dimension of one element is free
     a.k_sp = num_pages > 1 ? k_cache_strides[0] : kD, a.k_sh = Hkv > 1 ? k_cache_strides[1] : kD, a.k_sn = k_cache_strides[2];

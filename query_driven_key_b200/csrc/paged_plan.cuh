@@ -1,5 +1,5 @@
 // paged_plan.cuh -- how the attention of new tokens over the paged cache is
-// divided among the thread blocks, and the merge of what the division cut.
+// divided among the thread blocks, and how what the division cut is joined.
 //
 // Query rows: row r of request b is its new token r / G and query head r % G of
 // the KV head's group, so that the G heads that share keys fill a tile
@@ -9,11 +9,13 @@
 // form one sequence, requests first, then heads, then row tiles; block i of P
 // takes the i-th of P equal parts of it.  Whatever the mix of lengths, all blocks
 // get the same work to within a unit; an item that a part's border cuts is computed in
-// pieces, each piece leaves its (max, sum, O) in the workspace, and
-// merge_kernel joins them in order.  Lengths stay on the device: the plan is
+// pieces, each piece leaves its (max, sum, O) in the workspace, and the block
+// that finishes the last one joins them in order.  Lengths stay on the device: the plan is
 // recomputed from q_start and kv_lens by every launch, so that a captured
 // launch follows the lengths of each replay.
 #pragma once
+
+#include <type_traits>
 
 #include "pages.cuh"
 #include "ptx.cuh"
@@ -25,7 +27,8 @@ struct PagedArgs {
     void *out;
     const int32_t *q_start, *kv_lens, *table;
     unsigned *status;
-    float *part;  // [parts][2 pieces][sides][rows_cap][kPartLd]
+    unsigned *tickets;  // [parts] pieces of the item that a part begins which are done; zero between calls
+    float *part;  // [parts][2 pieces][sides] partials
     int64_t q_st, q_sh, o_st, o_sh;
     int64_t k_sp, k_sh, k_sn, v_sp, v_sh, v_sn;
     int64_t table_ld;
@@ -37,7 +40,7 @@ struct PagedArgs {
     float scale_log2;
 };
 
-constexpr int kPartLd = kD + 2;  // O[128], max, sum of a row
+constexpr int kPartLd = kD + 2;  // a partial: O [128 channels][rows_cap], maxima [rows_cap], sums [rows_cap]
 
 struct Request {
     int row0, n, kv;  // first row of q, new tokens, tokens with the new ones
@@ -131,11 +134,33 @@ struct PlanSmem {
     Place place;
 };
 
-// The total number of units and the place of unit first(total); all NT
-// threads call it.  Up to NT / 32 requests: a warp each, a lane a row tile (a
+// The sequence of `total` units in min(parts, total) parts, none of which is empty.
+struct Parts {
+    int64_t total, per;
+    int n, rem;
+    __device__ __forceinline__ Parts(int64_t units, int parts) : total(units)
+    {
+        n = (int)min((int64_t)parts, total);
+        per = n > 0 ? total / n : 0;
+        rem = (int)(total - per * n);
+    }
+    // first unit of part i; total for the parts behind the last one
+    __device__ __forceinline__ int64_t begin(int i) const { return i >= n ? total : per * i + rem * i / n; }
+    // the part that holds unit u < total
+    __device__ __forceinline__ int of(int64_t u) const
+    {
+        int i = min(n - 1, (int)((double)u * n / (double)total));
+        while (i > 0 && begin(i) > u) --i;
+        while (begin(i + 1) <= u) ++i;
+        return i;
+    }
+};
+
+// The division of the sequence, and (in sm->place) the place of part `part`'s
+// first unit; all NT threads call it.  Up to NT / 32 requests: a warp each, a lane a row tile (a
 // prompt has hundreds of row tiles); more: a thread each.
-template <int R, int BN, int NT, typename First>
-__device__ __forceinline__ int64_t plan(const PagedArgs &a, PlanSmem *sm, First first)
+template <int R, int BN, int NT>
+__device__ __forceinline__ Parts plan(const PagedArgs &a, PlanSmem *sm, int part)
 {
     static_assert(NT % 32 == 0 && NT <= 1024, "whole warps");
     constexpr int W = NT / 32;
@@ -154,7 +179,8 @@ __device__ __forceinline__ int64_t plan(const PagedArgs &a, PlanSmem *sm, First 
             if (w == warp) before = total;
             total += sm->ws[w];
         }
-        int64_t rem = first(total) - before;
+        const Parts parts(total, a.parts);
+        int64_t rem = parts.begin(part) - before;
         if (rem >= 0 && rem < uh * a.Hkv) {  // this warp's request holds the place
             Place p;
             p.b = warp;
@@ -178,7 +204,7 @@ __device__ __forceinline__ int64_t plan(const PagedArgs &a, PlanSmem *sm, First 
             }
         }
         __syncthreads();
-        return total;
+        return parts;
     }
     int64_t mine = 0, sum = 0;  // the last request of this thread, all of them
     for (int b = tid; b < a.B; b += NT) {
@@ -191,7 +217,8 @@ __device__ __forceinline__ int64_t plan(const PagedArgs &a, PlanSmem *sm, First 
     int64_t total = 0;
     for (int w = 0; w < W; ++w) total += sm->ws[w];
     __syncthreads();
-    const int64_t u = first(total);
+    const Parts parts(total, a.parts);
+    const int64_t u = parts.begin(part);
     int64_t base = 0;
     for (int b0 = 0; b0 < a.B && base <= u; b0 += NT) {
         const int b = b0 + tid;
@@ -224,15 +251,7 @@ __device__ __forceinline__ int64_t plan(const PagedArgs &a, PlanSmem *sm, First 
         base += chunk;
         __syncthreads();
     }
-    return total;
-}
-
-// First unit of part `part` of the min(parts, total) parts, none of which
-// is empty; total for the parts behind the last one.
-__device__ __forceinline__ int64_t part_begin(int64_t total, int part, int parts)
-{
-    const int64_t n = min((int64_t)parts, total);
-    return part >= n ? total : total / n * part + total % n * part / n;
+    return parts;
 }
 
 // Walk over the items of a part: the current item's piece [j0, j1) of key
@@ -242,13 +261,16 @@ struct Walk {
     const PagedArgs &a;
     Place p;
     Request s;
+    int64_t first;  // the item's first unit
     int64_t left;   // units of the part from the place on
     TileRange t;    // the item
     int j0, j1;     // the piece
     bool whole, head;  // head: the piece begins with the item
-    __device__ __forceinline__ Walk(const PagedArgs &args, const Place &place, int64_t units) : a(args), p(place), left(units)
+    __device__ __forceinline__ Walk(const PagedArgs &args, const Place &place, const Parts &parts, int part)
+        : a(args), p(place), first(parts.begin(part)), left(parts.begin(part + 1) - first)
     {
         if (left > 0) {
+            first -= p.off;
             s = load_request(a, p.b);
             set();
         }
@@ -265,10 +287,11 @@ struct Walk {
     __device__ __forceinline__ bool live() const { return left > 0; }
     __device__ __forceinline__ void assign(const Walk &o)
     {
-        p = o.p, s = o.s, left = o.left, t = o.t, j0 = o.j0, j1 = o.j1, whole = o.whole, head = o.head;
+        p = o.p, s = o.s, first = o.first, left = o.left, t = o.t, j0 = o.j0, j1 = o.j1, whole = o.whole, head = o.head;
     }
     __device__ __forceinline__ void next()
     {
+        first += kItemCost + t.j1 - t.j0;
         left -= kItemCost + t.j1 - t.j0 - p.off;
         if (left <= 0) return;
         p.off = 0;
@@ -297,121 +320,144 @@ __device__ __forceinline__ float *part_at(const PagedArgs &a, int part, int piec
     return a.part + ((int64_t)((part * 2 + piece) * a.sides + side)) * a.rows_cap * kPartLd;
 }
 
-template <typename T>
-__device__ __forceinline__ void store_out4(T *p, float4 x);
-template <>
-__device__ __forceinline__ void store_out4<float>(float *p, float4 x)
+// N neighbouring channels of an output row.
+template <int N>
+__device__ __forceinline__ void store_out(float *p, const float (&x)[N])
 {
-    *reinterpret_cast<float4 *>(p) = x;
+#pragma unroll
+    for (int i = 0; i < N; i += 2) *reinterpret_cast<float2 *>(p + i) = make_float2(x[i], x[i + 1]);
 }
-template <>
-__device__ __forceinline__ void store_out4<__nv_bfloat16>(__nv_bfloat16 *p, float4 x)
+template <int N>
+__device__ __forceinline__ void store_out(__nv_bfloat16 *p, const float (&x)[N])
 {
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(x.x, x.y), hi = __floats2bfloat162_rn(x.z, x.w);
-    *reinterpret_cast<uint2 *>(p) =
-        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-}
-
-// Join the pieces of the item that the border between parts c - 1 and c cuts,
-// if that is the first border inside the item (blockIdx.x = c - 1; the blocks
-// of one x share the rows):
-//     m = max m_i,  l = sum l_i 2^(m_i - m),  out = sum O_i 2^(m_i - m) / l.
-// A row that sees no key has l = 0 and gets zeros.  With fewer rows than warps
-// several warps share a row's partials (a decode step has few rows and up to
-// hundreds of partials each); the lanes of a warp read 32 (m, l) at once, and
-// the loads of the O_i do not wait for one another.  The order of the sums is
-// fixed, so that the result does not depend on timing.
-constexpr int kMergeThreads = 256;
-constexpr int kMergeSlices = 8;
-
-template <typename T, int R, int BN, bool TWO_SIDES>
-__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedArgs a)
-{
-    constexpr int W = kMergeThreads / 32;
-    __shared__ PlanSmem sm;
-    __shared__ __align__(16) float s_o[W][kD];
-    __shared__ float2 s_ml[W];
-    const int c = (int)blockIdx.x + 1;
-    const int64_t total = plan<R, BN, kMergeThreads>(a, &sm, [&](int64_t n) { return part_begin(n, c, a.parts); });
-    const int64_t u = part_begin(total, c, a.parts);
-    grid_dependency_wait();  // every block waits, so that this grid ends after the attention
-    if (u >= total) return;
-    const Place p = sm.place;
-    const int64_t start = u - p.off + kItemCost;  // the item's first key tile in the sequence
-    if (u <= start || part_begin(total, c - 1, a.parts) > start) return;
-    const Request s = load_request(a, p.b);
-    const TileRange t = tile_range<R, BN>(a, s, p.qt);
-    // the last part that holds a piece of the item: that of its last key tile
-    const int64_t end = start + (t.j1 - t.j0);
-    int lo = c, hi = a.parts - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (part_begin(total, mid, a.parts) < end) lo = mid;
-        else hi = mid - 1;
+    uint32_t w[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&b);
     }
+    if constexpr (N == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else *reinterpret_cast<uint32_t *>(p) = w[0];
+}
+
+// Join the pieces of an item, in the parts c0 .. c1:
+//     m = max m_i,  l = sum l_i 2^(m_i - m),  out = sum O_i 2^(m_i - m) / l.
+// A row that sees no key has l = 0 and gets zeros.  First m and l, with as many
+// lanes a row as 256 threads allow (a decode step has few rows and up to
+// hundreds of partials each), then eight channels of a row a thread (two with few
+// rows, so that more threads share the partials).  Rows are
+// the partials' fast dimension, so that neighbouring threads read neighbouring
+// words, and no load waits for another one.  The order of the sums is fixed, so
+// that the result does not depend on timing.  Called by 256 threads with sync()
+// as their barrier.
+constexpr int kMergeThreads = 256;
+struct MergeSmem {
+    float m[kMergeThreads], inv[kMergeThreads];  // of a row: maximum, 1 / sum
+    float g[1024];                               // of a partial and row, where they fit: 2^(m_i - m) / l
+};
+// The parts c0 .. c1 that hold pieces of an item; whether all others are done.
+struct Pieces {
+    int c0, c1, last;
+};
+
+template <typename W>
+__device__ __forceinline__ void find_pieces(Pieces &x, const Parts &parts, const W &w)
+{
+    const int64_t tile0 = w.first + kItemCost;  // the unit of the item's first key tile
+    x.c0 = parts.of(tile0);
+    x.c1 = parts.of(tile0 + (w.t.j1 - w.t.j0) - 1);
+}
+
+template <typename T, int R, bool TWO_SIDES, typename Sync>
+__device__ __forceinline__ void merge_pieces(const PagedArgs &a, MergeSmem &sm, const Pieces &x, const Request &s, const Place &p,
+                                             int tid, Sync sync)
+{
+    static_assert(R <= kMergeThreads, "a thread a row at least");
+    const int c0 = x.c0, c1 = x.c1;
     const int rows = min(R, s.n * a.group.d - p.qt * R);
     const bool two_sides = TWO_SIDES && rows <= R / 2;  // the two sides hold the same rows
-    const int count = (lo - c + 2) * (two_sides ? 2 : 1);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // rows blockIdx.y, blockIdx.y + kMergeSlices, ..., `share` warps a row
-    const int mine = (rows - (int)blockIdx.y + kMergeSlices - 1) / kMergeSlices;
-    const int share = mine >= W ? 1 : mine > 4 ? 1 : mine > 2 ? 2 : mine > 1 ? 4 : W;
-    for (int k0 = 0; k0 < mine; k0 += W / share) {
-        const int k = k0 + warp / share, r = (int)blockIdx.y + k * kMergeSlices;
-        const bool real = k < mine;
-        const int side0 = TWO_SIDES && !two_sides ? r / (R / 2) : 0;
-        const int row = TWO_SIDES && !two_sides ? r % (R / 2) : r;
-        auto partial = [&](int i) {
-            const int part = c - 1 + (two_sides ? i >> 1 : i);
-            return part_at(a, part, part == c - 1 ? 1 : 0, two_sides ? i & 1 : side0) + (int64_t)row * kPartLd;
-        };
-        float m = -INFINITY, l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (real)
-            for (int i0 = warp % share; i0 < count; i0 += 32 * share) {  // partials i0, i0 + share, ...
-                const int n = min(32, (count - i0 + share - 1) / share);
-                float2 ml = make_float2(-INFINITY, 0.f);
-                if (lane < n) ml = __ldcg(reinterpret_cast<const float2 *>(partial(i0 + lane * share) + kD));
-                float mn = ml.x;
+    const int count = (c1 - c0 + 1) * (two_sides ? 2 : 1);
+    // element x of partial i of row r
+    auto at = [&](int i, int r) {
+        const int part = c0 + (two_sides ? i >> 1 : i);
+        const int side = two_sides ? i & 1 : TWO_SIDES ? r / (R / 2) : 0;
+        return part_at(a, part, part == c0 ? 1 : 0, side) + (TWO_SIDES && !two_sides ? r % (R / 2) : r);
+    };
+    const int64_t ld = a.rows_cap;
+    int lanes = 32;  // of a row
+    while (rows * lanes > kMergeThreads) lanes >>= 1;
+    const bool kept = count <= 4 * lanes && count * rows <= 1024;
+    {
+        const int r = tid / lanes, i0 = tid % lanes;
+        float m = -INFINITY, l = 0.f, mi[4], li[4];
+        for (int ib = i0; ib < count; ib += 4 * lanes) {
 #pragma unroll
-                for (int d = 16; d > 0; d >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, d));
-                mn = fmaxf(mn, m);
-                const float ref = mn == -INFINITY ? 0.f : mn;
-                const float f = exp2f(m - ref), g = exp2f(ml.x - ref);
-                l = l * f + warp_sum(ml.y * g);
-                m = mn;
-                o.x *= f, o.y *= f, o.z *= f, o.w *= f;
-#pragma unroll 8
-                for (int i = 0; i < n; ++i) {
-                    const float *x = partial(i0 + i * share);
-                    const float2 a0 = __ldcg(reinterpret_cast<const float2 *>(x) + 2 * lane);
-                    const float2 a1 = __ldcg(reinterpret_cast<const float2 *>(x) + 2 * lane + 1);
-                    const float gi = __shfl_sync(0xffffffffu, g, i);
-                    o.x += a0.x * gi, o.y += a0.y * gi, o.z += a1.x * gi, o.w += a1.y * gi;
-                }
+            for (int u = 0; u < 4; ++u) {
+                const int i = ib + u * lanes;
+                mi[u] = -INFINITY, li[u] = 0.f;
+                if (i < count && r < rows) mi[u] = __ldcg(at(i, r) + kD * ld), li[u] = __ldcg(at(i, r) + (kD + 1) * ld);
             }
-        if (share > 1) {  // the row's first warp adds the others' sums in order
-            __syncthreads();
-            *reinterpret_cast<float4 *>(&s_o[warp][4 * lane]) = o;
-            if (lane == 0) s_ml[warp] = make_float2(m, l);
-            __syncthreads();
-            if (warp % share) continue;
-            for (int w = warp + 1; w < warp + share; ++w) {
-                const float2 y = s_ml[w];
-                const float4 q = *reinterpret_cast<const float4 *>(&s_o[w][4 * lane]);
-                const float mn = fmaxf(m, y.x), ref = mn == -INFINITY ? 0.f : mn;
-                const float f = exp2f(m - ref), g = exp2f(y.x - ref);
-                o.x = o.x * f + q.x * g, o.y = o.y * f + q.y * g, o.z = o.z * f + q.z * g, o.w = o.w * f + q.w * g;
-                l = l * f + y.y * g;
-                m = mn;
+            const float mn = fmaxf(fmaxf(fmaxf(mi[0], mi[1]), fmaxf(mi[2], mi[3])), m), ref = mn == -INFINITY ? 0.f : mn;
+            l *= exp2f(m - ref);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) l += li[u] * exp2f(mi[u] - ref);
+            m = mn;
+        }
+        float top = m;
+        for (int d = lanes >> 1; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const float ref = top == -INFINITY ? 0.f : top;
+        l *= exp2f(m - ref);
+        for (int d = lanes >> 1; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        if (r < rows) {
+            if (i0 == 0) sm.m[r] = ref, sm.inv[r] = inv;
+            if (kept) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (i0 + u * lanes < count) sm.g[(i0 + u * lanes) * rows + r] = exp2f(mi[u] - ref) * inv;
             }
         }
-        if (!real) continue;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        const int gr = p.qt * R + r, tok = a.group.quot(gr), g = gr - tok * a.group.d;
-        store_out4(static_cast<T *>(a.out) + (int64_t)(s.row0 + tok) * a.o_st + (int64_t)(p.h * a.group.d + g) * a.o_sh + 4 * lane,
-                   make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     }
+    sync();
+    auto channels = [&](auto width) {
+        constexpr int N = decltype(width)::value;
+        for (int k = tid; k < rows * (kD / N); k += kMergeThreads) {
+            const int c = k / rows * N, r = k % rows;
+            const float m = sm.m[r], inv = sm.inv[r];
+            float o[N];
+#pragma unroll
+            for (int j = 0; j < N; ++j) o[j] = 0.f;
+#pragma unroll(32 / N)
+            for (int i = 0; i < count; ++i) {
+                const float *x = at(i, r);
+                const float g = kept ? sm.g[i * rows + r] : exp2f(__ldcg(x + kD * ld) - m) * inv;
+#pragma unroll
+                for (int j = 0; j < N; ++j) o[j] += __ldcg(x + (c + j) * ld) * g;
+            }
+            const int gr = p.qt * R + r, tok = a.group.quot(gr), g = gr - tok * a.group.d;
+            store_out(static_cast<T *>(a.out) + (int64_t)(s.row0 + tok) * a.o_st + (int64_t)(p.h * a.group.d + g) * a.o_sh + c, o);
+        }
+    };
+    if (rows > 4) channels(std::integral_constant<int, 8>{});
+    else channels(std::integral_constant<int, 2>{});
+}
+
+// A piece's partial has been written by the calling 256 threads: count it, and
+// join the item's pieces if it was the last one.  `x` (shared) comes from
+// find_pieces.  The counters are in the workspace, one a part (a part begins at
+// most one item that another one ends), and are zero again when the item is
+// done.
+template <typename T, int R, bool TWO_SIDES, typename W, typename Sync>
+__device__ __forceinline__ void finish_piece(const PagedArgs &a, MergeSmem &sm, Pieces &x, const W &w, int tid, Sync sync)
+{
+    sync();
+    if (tid == 0) {
+        x.last = atom_add_acq_rel_gpu(a.tickets + x.c0, 1u) == (unsigned)(x.c1 - x.c0);
+        if (x.last) a.tickets[x.c0] = 0u;
+    }
+    sync();
+    if (x.last) merge_pieces<T, R, TWO_SIDES>(a, sm, x, w.s, w.p, tid, sync);
+    sync();
 }
 
 }  // namespace think

@@ -15,7 +15,7 @@
 
 namespace think {
 
-constexpr int kSimtThreads = 256;
+constexpr int kSimtThreads = kMergeThreads;
 constexpr int kSimtBN = 64;
 
 template <int R>
@@ -39,17 +39,16 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedArg
     extern __shared__ __align__(16) float smem[];
     float *qs = smem, *ks = qs + R * kD, *vs = ks + BN * kD, *ps = vs + BN * kD;  // ps: [BN][R]
     __shared__ PlanSmem sm;
+    __shared__ Pieces pieces;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     grid_dependency_wait();
     const int part = blockIdx.x;
-    const int64_t total =
-        plan<R, BN, kSimtThreads>(a, &sm, [&](int64_t n) { return part_begin(n, part, a.parts); });
+    const Parts parts = plan<R, BN, kSimtThreads>(a, &sm, part);
     grid_launch_dependents();
-    const int64_t u0 = part_begin(total, part, a.parts), u1 = part_begin(total, part + 1, a.parts);
-    if (u0 >= u1) return;
-    for (Walk<R, BN> w(a, sm.place, u1 - u0); w.live(); w.next()) {
+    for (Walk<R, BN> w(a, sm.place, parts, part); w.live(); w.next()) {
         const int rows = min(R, w.s.n * a.group.d - w.p.qt * R);
         __syncthreads();  // the previous item's tiles have been read
+        if (!w.whole && tid == 0) find_pieces(pieces, parts, w);
         for (int i = tid; i < R * 32; i += kSimtThreads) {
             const int r = i >> 5, c4 = i & 31;
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -159,15 +158,18 @@ __global__ void __launch_bounds__(kSimtThreads) paged_simt_kernel(const PagedArg
                 const int gr = w.p.qt * R + r, tok = a.group.quot(gr), g = gr - tok * a.group.d;
                 float *dst = static_cast<float *>(a.out) + (int64_t)(w.s.row0 + tok) * a.o_st +
                              (int64_t)(w.p.h * a.group.d + g) * a.o_sh + 4 * tx;
-                store_out4(dst, make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv));
-                store_out4(dst + 64, make_float4(o[i][4] * inv, o[i][5] * inv, o[i][6] * inv, o[i][7] * inv));
+                *reinterpret_cast<float4 *>(dst) = make_float4(o[i][0] * inv, o[i][1] * inv, o[i][2] * inv, o[i][3] * inv);
+                *reinterpret_cast<float4 *>(dst + 64) = make_float4(o[i][4] * inv, o[i][5] * inv, o[i][6] * inv, o[i][7] * inv);
             } else {
-                float *dst = part_at(a, part, w.head ? 1 : 0, 0) + (int64_t)r * kPartLd;
+                float *dst = part_at(a, part, w.head ? 1 : 0, 0) + r;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) dst[4 * tx + j] = o[i][j], dst[64 + 4 * tx + j] = o[i][4 + j];
-                if (tx == 0) dst[kD] = m[i], dst[kD + 1] = s;
+                for (int j = 0; j < 4; ++j)
+                    dst[(4 * tx + j) * a.rows_cap] = o[i][j], dst[(64 + 4 * tx + j) * a.rows_cap] = o[i][4 + j];
+                if (tx == 0) dst[kD * a.rows_cap] = m[i], dst[(kD + 1) * a.rows_cap] = s;
             }
         }
+        if (!w.whole)
+            finish_piece<float, R, false>(a, *reinterpret_cast<MergeSmem *>(vs), pieces, w, tid, [] { __syncthreads(); });
     }
 }
 

@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     __shared__ PlanSmem plan_sm;
     __shared__ PtBars bars;
     __shared__ float2 s_ml[128];  // split items: (m, l) of warpgroup 1
+    __shared__ Pieces pieces;
     unsigned char *qs = smem, *ring = smem + 2 * kPtTile;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile uint32_t *abort_flag = &bars.abort_flag;
@@ -218,10 +219,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     }
     grid_dependency_wait();
     const int part = blockIdx.x;
-    const int64_t total =
-        plan<kPtRows, kPtBN, kPtThreads>(a, &plan_sm, [&](int64_t n) { return part_begin(n, part, a.parts); });
+    const Parts parts = plan<kPtRows, kPtBN, kPtThreads>(a, &plan_sm, part);
     grid_launch_dependents();
-    const int64_t units = part_begin(total, part + 1, a.parts) - part_begin(total, part, a.parts);
     tc05::fence_before_sync();
     __syncthreads();
     tc05::fence_after_sync();
@@ -239,7 +238,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         uint32_t ld = 0;                     // loads issued: stage ld % kPtStages
         uint32_t phases = 0, used = 0;       // of each full barrier its next phase; of each stage the last one's set
         bool ok = true;
-        for (W w(a, place, units); w.live() && ok; w.next()) {
+        for (W w(a, place, parts, part); w.live() && ok; w.next()) {
             const PtItem x = pt_item(a, w);
             const PtOrder order{x.split ? 2 : 1, x.n};
             // this lane's rows of load i: the table entry (-1: no key of them is
@@ -308,7 +307,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const uint64_t v_desc = tc05::smem_desc(smem_addr(ring), 16384u, 1024u, tc05::kLayoutSwizzle128B);
         const uint32_t s_tmem = uniform(tmem + 128u * t), o_tmem = s_tmem + 256u;
         const uint32_t s_bar = uniform(sfull0 + 8 * t), o_bar = uniform(ofull0 + 8 * t);
-        for (W w(a, place, units); w.live() && ok; w.next()) {
+        for (W w(a, place, parts, part); w.live() && ok; w.next()) {
             const PtItem x = pt_item(a, w);
             const PtOrder order{x.split ? 2 : 1, x.n};
             const int j0 = x.split ? t : 0, step = x.split ? 2 : 1;
@@ -448,7 +447,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(qfull0 + (x.split ? 16 : 8 * t));
         };
-        W w(a, place, units);
+        W w(a, place, parts, part);
         if (w.live()) load_q(w);
         while (w.live()) {
             const PtItem x = pt_item(a, w);
@@ -459,6 +458,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             // (a row that is not real takes part as the last one of its request: what it holds is not stored)
             const int tok = a.group.quot(row);
             const int pos = base + (real ? tok : w.s.n - 1);
+            if (!w.whole && tid == 0) find_pieces(pieces, parts, w);
             float m = -INFINITY, l = 0.f;
             const int step = x.split ? 2 : 1, j0 = x.split ? t : 0;
             for (int j = j0; j < x.n; j += step) {
@@ -545,11 +545,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             const bool any = j0 < x.n;  // this warpgroup had key tiles
             const bool join = x.split && w.whole && x.n > 1;
-            // the next item's Q, unless the second Q tile is used below: its
-            // first products then run beside this item's end
+            // the next item's Q, unless it needs the second Q tile while that is
+            // used below: its first products then run beside this item's end
             W nx = w;
             nx.next();
-            if (!join && nx.live()) load_q(nx);
+            const bool late = (join || !w.whole) && nx.live() && !pt_item(a, nx).split;
+            if (!late && nx.live()) load_q(nx);
             if (any) wait(ofull0 + 8 * t, no++);
             tc05::fence_after_sync();
             auto load_o = [&](int i, uint32_t (&o)[32]) {
@@ -611,7 +612,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
             } else if (warp_real && (any || !w.whole)) {
                 const float inv = l > 0.f ? 1.f / l : 0.f;
-                float *pt = part_at(a, part, w.head ? 1 : 0, t) + (int64_t)r * kPartLd;
+                float *pt = part_at(a, part, w.head ? 1 : 0, t) + r;  // element x of the row at pt[x * rows_cap]
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
                     uint32_t o[32];
@@ -624,15 +625,16 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         store_o(i, y, inv);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2)
-                            *reinterpret_cast<float2 *>(pt + 32 * i + c) =
-                                make_float2(__uint_as_float(o[c]), __uint_as_float(o[c + 1]));
+                        for (int c = 0; c < 32; ++c) pt[(32 * i + c) * a.rows_cap] = __uint_as_float(o[c]);
                     }
                 }
-                if (real && !w.whole) *reinterpret_cast<float2 *>(pt + kD) = make_float2(m * sl, l);
+                if (real && !w.whole) pt[kD * a.rows_cap] = m * sl, pt[(kD + 1) * a.rows_cap] = l;
             }
             tc05::fence_before_sync();
-            if (join && nx.live()) load_q(nx);
+            if (!w.whole)
+                finish_piece<__nv_bfloat16, kPtRows, true>(a, *reinterpret_cast<MergeSmem *>(qs + kPtTile), pieces, w, tid,
+                                                           [] { named_barrier(2, 256); });
+            if (late) load_q(nx);
             w.assign(nx);
         }
     }

@@ -23,9 +23,9 @@ def ws(n):
 
 
 def attn_ws(T, Hq, Hkv, dtype):
-    """A workspace whose scratch holds NaN: only the status word has to be zero."""
+    """A workspace whose scratch holds NaN: only the status word and the counters have to be zero."""
     w = torch.full((qdk.think_paged_attn_workspace_size(T, Hq, Hkv, dtype=dtype),), 255, dtype=torch.uint8, device="cuda")
-    w[:256] = 0
+    w[:256 + 2048] = 0
     return w
 
 
