@@ -26,8 +26,8 @@
 // Value rows behind the request's last token are set to zero in shared memory
 // before their product, whatever the page holds there.
 //
-// Warps: 8 softmax, 1 producer (a lane a load), 2 for the products (a warpgroup
-// each; the first owns the TMEM), 1 idle.  TMEM columns: S_t (and P_t in its first half) at 128 t, O_t at
+// Warps: 8 softmax, 2 producers, 2 for the products (a warpgroup each; the first
+// owns the TMEM).  TMEM columns: S_t (and P_t in its first half) at 128 t, O_t at
 // 256 + 128 t.  Every wait is bounded; one that runs out sets the status bit and
 // the block's abort flag, after which every wait returns at once and all warps
 // still reach the final barrier, where the TMEM is released.
@@ -41,7 +41,7 @@ namespace think {
 
 constexpr int kPtRows = 256;
 constexpr int kPtBN = 128;
-constexpr int kPtThreads = 384;  // 12 warps: the last one only lends its registers
+constexpr int kPtThreads = 384;
 constexpr int kPtProducer = 8;
 constexpr int kPtMma = 9;
 constexpr int kPtStages = 5;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const uint32_t full0 = smem_addr(bars.full), empty0 = smem_addr(bars.empty), qfull0 = smem_addr(bars.q_full),
                    sfull0 = smem_addr(bars.s_full), pfull0 = smem_addr(bars.p_full), ofull0 = smem_addr(bars.o_full), turn0 = smem_addr(bars.turn), done = smem_addr(&bars.done);
     if (tid == 0) {
-        for (int s = 0; s < 3 * kPtStages; ++s) mbar_init(full0 + 8 * s, 1);
+        for (int s = 0; s < 3 * kPtStages; ++s) mbar_init(full0 + 8 * s, 2);
         for (int s = 0; s < kPtStages; ++s) mbar_init(empty0 + 8 * s, 2);
         mbar_init(qfull0 + 16, 8);
         for (int t = 0; t < 2; ++t) {
@@ -231,9 +231,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     // = 256 x 216 for the softmax warps + 128 x 72 for the others.
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == kPtProducer) {
-        // ---------------------------------------------------------- producer
-        const int per_tile = kPtBN / chunk;  // loads of one 64-channel half
+    if (warp == kPtProducer || warp == kPtMma + 2) {
+        // --------------------------------------------------------- producers
+        // A warp a 64-channel half, a lane a chunk: a warp's lanes issue their
+        // loads one after another, and with 16-row pages a tile has 8 of each half.
+        const int half = warp != kPtProducer;
+        const int per_tile = kPtBN / chunk;
         const uint32_t bytes = (uint32_t)chunk * 128u;
         uint32_t ld = 0;                     // loads issued: stage ld % kPtStages
         uint32_t phases = 0, used = 0;       // of each full barrier its next phase; of each stage the last one's set
@@ -246,8 +249,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             // row in the page
             auto locate = [&](int i, int &entry, int &row, bool &needed, bool &value, int &tile) {
                 tile = order.tile(i, value);
-                const int key = (w.j0 + tile) * kPtBN + (lane >> 1) * chunk;
-                needed = (lane >> 1) < per_tile && key < w.t.hi && key + chunk > w.t.lo;
+                const int key = (w.j0 + tile) * kPtBN + lane * chunk;
+                needed = lane < per_tile && key < w.t.hi && key + chunk > w.t.lo;
                 const int j = a.page.quot(key);
                 row = key - j * a.page.d;
                 entry = needed ? a.table[(int64_t)w.p.b * a.table_ld + j] : -1;
@@ -266,13 +269,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 const uint32_t set = x.split ? 1u + (cur_tile & 1) : 0u, full = full0 + 8 * (set * kPtStages + s);
                 phases ^= 1u << (set * kPtStages + s);
                 used = (used & ~(3u << (2 * s))) | set << (2 * s);
-                if (lane == 0) mbar_arrive_expect_tx(full, kPtTile);
+                if (lane == 0) mbar_arrive_expect_tx(full, kPtTile / 2);
                 __syncwarp();
-                if ((lane >> 1) < per_tile) {
+                if (lane < per_tile) {
                     const bool inside = cur_needed && (unsigned)cur_entry < (unsigned)a.num_pages;
                     if (cur_needed && !inside) atomicOr(a.status, THINK_DEVICE_BAD_PAGE);
-                    tma_load_4d(smem_addr(ring + s * kPtTile) + (uint32_t)(lane & 1) * 16384u + (uint32_t)(lane >> 1) * bytes,
-                                cur_value ? &tm_v : &tm_k, (lane & 1) * 64, inside ? cur_row : 0, w.p.h,
+                    tma_load_4d(smem_addr(ring + s * kPtTile) + (uint32_t)half * 16384u + (uint32_t)lane * bytes,
+                                cur_value ? &tm_v : &tm_k, half * 64, inside ? cur_row : 0, w.p.h,
                                 inside ? cur_entry : a.num_pages, full);
                 }
             }
