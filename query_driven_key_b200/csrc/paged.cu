@@ -160,11 +160,17 @@ think_status_t think_extend_pages(const int32_t *new_lens, const int32_t *kv_len
     a.B = B;
     a.page = Divisor(page_size);
     a.n_free = n_free;
-    // one block for a decode step's few rows; up to a cluster of eight for prompts
+    a.in_place = kv_lens_out == kv_lens || free_count_out == free_count;
+    // A decode step's few requests and rows: one small block.  Prompts: a block
+    // for every 4096 rows (four a thread); at most the eight of a cluster in place.
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (B <= kPagesThreadsFew && T <= 4 * kPagesThreadsFew) {
+        return launch_pdl(extend_pages_kernel<kPagesThreadsFew>, dim3(1), dim3(kPagesThreadsFew), 0, st, a);
+    }
     int blocks = 1;
-    while (blocks < kPagesMaxCluster && T > blocks * kExtendRowsPerBlock) blocks *= 2;
-    return launch_pdl_cluster(extend_pages_kernel, dim3((unsigned)blocks), dim3(kPagesThreads), 0,
-                              static_cast<cudaStream_t>(stream), blocks, a);
+    while (blocks < (a.in_place ? 8 : 32) && T > blocks * kExtendRowsPerBlock) blocks *= 2;
+    return launch_pdl_cluster(extend_pages_kernel<kPagesThreads>, dim3((unsigned)blocks), dim3(kPagesThreads), 0, st,
+                              a.in_place ? blocks : 0, a);
 }
 
 think_status_t think_norm_rope_append(const void *q, const int64_t q_strides[2], const void *k, const int64_t k_strides[2],

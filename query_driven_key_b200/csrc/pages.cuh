@@ -12,8 +12,7 @@
 
 namespace think {
 
-constexpr int kPagesThreads = 1024;
-constexpr int kPagesMaxCluster = 8;
+constexpr int kPagesThreads = 1024, kPagesThreadsFew = 256;
 constexpr int kMaxPosition = 1 << 30;  // positions and lengths stay below, so that tile arithmetic fits 32 bits
 
 // Quotients by a divisor that a launch fixes, of dividends in [0, 2^31): the
@@ -40,10 +39,11 @@ struct ExtendArgs {
     int64_t table_ld, T, limit;  // limit: the tokens that a table row can hold
     Divisor page;
     int B, n_free;
+    bool in_place;  // an output is its own input: the blocks form a cluster
 };
 
-// Inclusive scan of one value a thread over the block (kPagesThreads
-// threads); *total receives the block's sum.  `ws` holds 33 words.
+// Inclusive scan of one value a thread over the block (NT threads); *total receives the block's sum.  `ws` holds 33 words.
+template <int NT>
 __device__ __forceinline__ int64_t block_scan_i64(int64_t x, int64_t *ws, int64_t *total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -55,108 +55,135 @@ __device__ __forceinline__ int64_t block_scan_i64(int64_t x, int64_t *ws, int64_
     if (lane == 31) ws[warp] = x;
     __syncthreads();
     if (warp == 0) {
-        int64_t s = ws[lane];
+        int64_t s = lane < NT / 32 ? ws[lane] : 0;
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
+        for (int d = 1; d < NT / 32; d <<= 1) {
             const int64_t y = __shfl_up_sync(0xffffffffu, s, d);
             if (lane >= d) s += y;
         }
-        ws[lane] = s;
+        if (lane < NT / 32) ws[lane] = s;
     }
     __syncthreads();
     x += warp ? ws[warp - 1] : 0;
-    *total = ws[31];
+    *total = ws[NT / 32 - 1];
     __syncthreads();
     return x;
 }
 
-// Every block of the (one) cluster scans the requests, 1024 at a time, and
-// keeps their row range, length and place in the free stack in shared memory;
-// then the cluster's threads share the new tokens: each finds its request by
-// binary search and writes its position and slot.  A page is fresh exactly
-// where its first row is a new token, so that token's thread writes the table
-// entry, and no thread reads an entry that another one writes.  kv_lens and
-// free_count may be the outputs themselves: every block has read a chunk's
-// lengths before block 0 writes them (cluster barrier).  Bound by latency: a
-// few dependent loads, a scan of ten shuffles and the slot stores.
-__global__ void __launch_bounds__(kPagesThreads) extend_pages_kernel(const ExtendArgs a)
+// Every block scans the requests, NT at a time, and keeps their row range,
+// length and place in the free stack in shared memory; then the blocks share
+// the new tokens, four neighbouring ones each:
+// a binary search finds the first one's request, the others follow it, and
+// positions and slots leave as vectors.  A page is fresh exactly where its first
+// row is a new token, so that token's thread writes the table entry, and no
+// thread reads an entry that another one writes.  kv_lens and free_count may be
+// the outputs themselves: the blocks are then one cluster, and every block has
+// read a chunk's lengths before block 0 writes them.  Bound by latency: a few dependent loads, two
+// scans of ten shuffles and the stores.
+template <int NT>
+__global__ void __launch_bounds__(NT, 1) extend_pages_kernel(const ExtendArgs a)
 {
     __shared__ int64_t ws[33];
-    __shared__ int64_t s_row[kPagesThreads + 1];   // first row of the request
-    __shared__ int s_len[kPagesThreads];           // tokens before
-    __shared__ int64_t s_free[kPagesThreads];      // pages handed out before it; -1: not admitted
+    __shared__ int s_row[NT + 1];  // first row of the request, held to T
+    __shared__ int s_len[NT];      // tokens before
+    __shared__ int s_free[NT];     // pages handed out before it; -1: not admitted
+    __shared__ int s_used;                    // pages of the admitted requests
     const int tid = threadIdx.x;
     const int rank = (int)blockIdx.x, blocks = (int)gridDim.x;
+    if (tid == 0) s_used = 0;
     grid_dependency_wait();
-    const int64_t count = min(max(*a.free_count, 0), a.n_free);
-    int64_t rows = 0, pages = 0, used = 0;  // over the chunks so far; used: pages of the admitted requests
+    const int count = min(max(*a.free_count, 0), a.n_free);
+    const bool vectors = (((uintptr_t)a.positions | (uintptr_t)a.slots) & 15u) == 0;
+    const int T = (int)a.T;
+    int64_t rows = 0, pages = 0;  // over the chunks so far
     unsigned bits = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kPagesThreads) {
+    for (int b0 = 0; b0 < a.B; b0 += NT) {
         const int b = b0 + tid;
         const bool real = b < a.B;
         const int n = real ? min(max(a.new_lens[b], 0), kMaxPosition) : 0;
         const int len = real ? min(max(a.kv_lens[b], 0), kMaxPosition) : 0;
         int64_t total, taken;
-        const int64_t row_end = rows + block_scan_i64(n, ws, &total);
+        const int64_t row_end = rows + block_scan_i64<NT>(n, ws, &total);
         // a request whose tokens do not fit its table row or the row arrays takes no page
         const bool fits = (int64_t)len + n <= a.limit && row_end <= a.T;
         const int need = fits ? a.page.quot(len + n + a.page.d - 1) - a.page.quot(len + a.page.d - 1) : 0;
-        const int64_t page_end = pages + block_scan_i64(need, ws, &taken);
+        const int64_t page_end = pages + block_scan_i64<NT>(need, ws, &taken);
         const bool admitted = fits && (need == 0 || page_end <= count);
-        s_row[tid] = row_end - n;
+        s_row[tid] = (int)min(row_end - n, a.T);
         s_len[tid] = len;
-        s_free[tid] = admitted ? page_end - need : -1;
-        if (tid == kPagesThreads - 1) s_row[kPagesThreads] = row_end;
+        s_free[tid] = admitted ? (int)min(page_end - need, (int64_t)count) : -1;
+        if (tid == NT - 1) s_row[NT] = (int)min(row_end, a.T);
         if (real && !admitted && n > 0) bits |= THINK_DEVICE_NO_PAGES;
-        // pages of the admitted requests: the needy ones among them are a prefix
-        int64_t dummy;
-        block_scan_i64(admitted ? need : 0, ws, &dummy);
-        used += dummy;
-        cluster_sync_all();  // (and a block barrier) every block has read this chunk's lengths
+        // (the admitted requests that want pages are a prefix of those that fit and want some)
+        const int used = __reduce_max_sync(0xffffffffu, admitted && need > 0 ? (int)page_end : 0);
+        if ((tid & 31) == 0 && used > 0) atomicMax(&s_used, used);
+        if (a.in_place) cluster_sync_all();  // every block has read this chunk's lengths
+        __syncthreads();
         if (rank == 0 && real) {
             a.kv_lens_out[b] = admitted ? len + n : len;
-            a.q_start[b] = (int32_t)min(row_end - n, a.T);
+            a.q_start[b] = s_row[tid];
             if (b == a.B - 1) a.q_start[a.B] = (int32_t)min(row_end, a.T);
         }
-        const int64_t lo = min(s_row[0], a.T), hi = min(s_row[kPagesThreads], a.T);
-        for (int64_t r = lo + (int64_t)rank * kPagesThreads + tid; r < hi; r += (int64_t)blocks * kPagesThreads) {
-            // the last request whose first row is <= r: it holds r (empty requests before it start there too)
-            int l = 0, h = kPagesThreads - 1;
+        const int lo = s_row[0], hi = s_row[NT];
+        for (int64_t g = (lo >> 2) + (int64_t)rank * NT + tid; 4 * g < hi; g += (int64_t)blocks * NT) {
+            const int r0 = max(lo, (int)(4 * g)), r1 = min(hi, (int)min(4 * g + 4, (int64_t)T));
+            // the last request whose first row is <= r0: it holds r0 (empty requests before it start there too)
+            int l = 0, h = NT - 1;
             while (l < h) {
                 const int m = (l + h + 1) >> 1;
-                if (s_row[m] <= r) l = m;
+                if (s_row[m] <= r0) l = m;
                 else h = m - 1;
             }
-            const int len0 = s_len[l];
-            const int pos = len0 + (int)(r - s_row[l]);
-            int64_t slot = -1;
-            if (s_free[l] >= 0) {
-                const int j = a.page.quot(pos), before = a.page.quot(len0 + a.page.d - 1);
-                int64_t at = (int64_t)(b0 + l) * a.table_ld + j;
-                int page;
-                if (j < before) {
-                    page = a.table[at];
-                } else {
-                    page = a.free_pages[count - 1 - (s_free[l] + (j - before))];
-                    if (pos - j * a.page.d == 0) a.table[at] = page;
+            int pos[4];
+            int64_t slot[4];
+            int at_l = -1, at_j = -1, page = -1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = r0 + i;
+                pos[i] = 0, slot[i] = -1;
+                if (r >= r1) continue;
+                while (l < NT - 1 && s_row[l + 1] <= r) ++l;
+                const int len0 = s_len[l];
+                pos[i] = len0 + (r - s_row[l]);
+                if (s_free[l] >= 0) {
+                    const int j = a.page.quot(pos[i]);
+                    if (l != at_l || j != at_j) {
+                        const int before = a.page.quot(len0 + a.page.d - 1);
+                        const int64_t at = (int64_t)(b0 + l) * a.table_ld + j;
+                        if (j < before) {
+                            page = a.table[at];
+                        } else {
+                            page = a.free_pages[count - 1 - (s_free[l] + (j - before))];
+                            if (pos[i] - j * a.page.d == 0) a.table[at] = page;
+                        }
+                        at_l = l, at_j = j;
+                    }
+                    if (page >= 0) slot[i] = (int64_t)page * a.page.d + (pos[i] - j * a.page.d);
+                    else bits |= THINK_DEVICE_BAD_PAGE;
                 }
-                if (page >= 0) slot = (int64_t)page * a.page.d + (pos - j * a.page.d);
-                else bits |= THINK_DEVICE_BAD_PAGE;
             }
-            a.positions[r] = pos;
-            a.slots[r] = slot;
+            if (vectors && r1 - r0 == 4) {
+                *reinterpret_cast<int4 *>(a.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+                *reinterpret_cast<longlong2 *>(a.slots + r0) = make_longlong2(slot[0], slot[1]);
+                *reinterpret_cast<longlong2 *>(a.slots + r0 + 2) = make_longlong2(slot[2], slot[3]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (r0 + i < r1) a.positions[r0 + i] = pos[i], a.slots[r0 + i] = slot[i];
+            }
         }
         rows += total;
         pages += taken;
         __syncthreads();  // the shared arrays are rewritten
     }
     // rows behind the last request
-    for (int64_t r = min(rows, a.T) + (int64_t)rank * kPagesThreads + tid; r < a.T; r += (int64_t)blocks * kPagesThreads) {
+    for (int64_t r = min(rows, a.T) + (int64_t)rank * NT + tid; r < a.T; r += (int64_t)blocks * NT) {
         a.positions[r] = 0;
         a.slots[r] = -1;
     }
-    cluster_sync_all();  // every block has read free_count
-    if (rank == 0 && tid == 0) *a.free_count_out = (int32_t)(count - used);
+    if (a.in_place) cluster_sync_all();  // every block has read free_count
+    else __syncthreads();
+    if (rank == 0 && tid == 0) *a.free_count_out = count - s_used;
     if (bits) atomicOr(a.status, bits);
 }
 
