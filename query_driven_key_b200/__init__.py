@@ -691,3 +691,71 @@ class PrunedCache:
                        _strides3(v), self.idx.data_ptr(), _dtype(q),
                        float(1.0 / float(d) ** 0.5 if scale is None else scale),
                        self.decode_ws.data_ptr(), self.decode_ws.numel(), self.k_pruned.device.index)
+
+
+class PagedCache:
+    """Pages of a batch of requests, shared by `layers` layers' pools, with the
+    tables of the current step.  Allocates with torch on construction, then
+    only calls the C entry points (release moves a request's page numbers with
+    torch).  A step: extend once, then append and attend in each layer; prune
+    hands a request over to the channel pruning."""
+
+    def __init__(self, B: int, Hq: int, Hkv: int, num_pages: int, page_size: int, max_blocks: int, max_rows: int,
+                 layers: int = 1, d: int = 128, dtype: torch.dtype = torch.bfloat16, device="cuda"):
+        self.B, self.Hq, self.Hkv, self.d, self.dtype = B, Hq, Hkv, d, dtype
+        self.num_pages, self.page_size, self.max_blocks = num_pages, page_size, max_blocks
+        new = lambda *shape, dt=torch.int32: torch.zeros(shape, dtype=dt, device=device)
+        self.k_cache = [new(num_pages, Hkv, page_size, d, dt=dtype) for _ in range(layers)]
+        self.v_cache = [new(num_pages, Hkv, page_size, d, dt=dtype) for _ in range(layers)]
+        self.block_table = new(B, max_blocks).fill_(-1)
+        self._stack = new(num_pages + max_blocks)  # (room behind the stack for release)
+        self._stack[:num_pages] = torch.arange(num_pages - 1, -1, -1, dtype=torch.int32)
+        self.free_pages, self.free_count = self._stack[:num_pages], new(1).fill_(num_pages)
+        self.kv_lens, self.q_start = new(B), new(B + 1)
+        self._positions, self._slots = new(max_rows), new(max_rows, dt=torch.int64)
+        self.positions, self.slots = self._positions, self._slots
+        self.extend_ws = new(think_extend_pages_workspace_size(), dt=torch.uint8)
+        self.attn_ws = new(max(256, think_paged_attn_workspace_size(max_rows, Hq, Hkv, d, dtype)), dt=torch.uint8)
+
+    def extend(self, new_lens, rows: int | None = None, stream=None):
+        """new_lens [B] int32 new tokens of each request -> lengths, tables, positions and slots of this step's `rows`
+        rows (default: max_rows; rows behind the last request get slot -1)."""
+        self.positions, self.slots = (self._positions, self._slots) if rows is None else \
+            (self._positions[:rows], self._slots[:rows])
+        think_extend_pages(new_lens, self.kv_lens, self.block_table, self.free_pages, self.free_count, self.page_size,
+                           self.kv_lens, self.free_count, self.q_start, self.positions, self.slots, self.extend_ws, stream)
+
+    def append(self, q, k, v, q_out, q_weight=None, k_weight=None, eps: float = 1e-6, inv_freq=None,
+               neighbours: bool = False, layer: int = 0, stream=None):
+        """This step's q, k, v rows: q normed and turned to q_out, k (normed, turned) and v to the pages."""
+        think_norm_rope_append(q, k, v, q_weight, k_weight, eps, inv_freq, neighbours, self.positions, self.slots, q_out,
+                               self.k_cache[layer], self.v_cache[layer], stream)
+
+    def attend(self, q, out, window: int = 0, scale: float | None = None, max_new: int = 0, layer: int = 0, stream=None):
+        """Attention of this step's rows (after append) over their requests' pages."""
+        think_paged_attn(q, self.k_cache[layer], self.v_cache[layer], self.block_table, self.q_start, self.kv_lens, out,
+                         self.attn_ws, window, scale, max_new, stream)
+
+    def gather(self, b: int, N: int, layer: int = 0, stream=None):
+        """The first N tokens of request b, contiguous: k, v [1,Hkv,N,d]."""
+        out = [torch.empty((1, self.Hkv, N, self.d), dtype=self.dtype, device=self.kv_lens.device) for _ in range(2)]
+        for cache, o in zip((self.k_cache[layer], self.v_cache[layer]), out):
+            think_gather_pages(cache, self.block_table[b:b + 1], self.kv_lens[b:b + 1], o, stream)
+        return out
+
+    def prune(self, b: int, N: int, q_win, T: int, layer: int = 0, stream=None):
+        """Request b, N tokens long, pruned to T key channels by its window queries q_win [1,Hq,S,d]: a PrunedCache and
+        the values [1,Hkv,N,d] for its decode."""
+        k, v = self.gather(b, N, layer, stream)
+        pruned = PrunedCache(1, self.Hq, self.Hkv, N, T, self.d, dtype=self.dtype, device=k.device)
+        pruned.prune(q_win, k, stream)
+        return pruned, v
+
+    def release(self, b: int):
+        """Request b is done: its pages go back to the stack, its length to 0 (on the current stream)."""
+        j = torch.arange(self.max_blocks, device=self.kv_lens.device)
+        n = (self.kv_lens[b] + self.page_size - 1) // self.page_size
+        self._stack[torch.where(j < n, self.free_count + j, self.num_pages + j)] = self.block_table[b]
+        self.free_count += n
+        self.kv_lens[b] = 0
+        self.block_table[b] = -1

@@ -38,7 +38,8 @@ __device__ __forceinline__ void cp_async_16_or_0(uint32_t dst, const void *src, 
 }
 
 // Element 4 c4 of row n of a 128-wide fp32 tile whose 16-byte vectors are
-// permuted within 8 rows, so that 8 rows' equal columns lie in 8 bank groups.
+// permuted within 8 rows, so that 8 rows' equal columns lie in 8 bank groups
+// (in Q, within 8 threads' rows: a warp reads those of two at once).
 __device__ __forceinline__ int swz(int n, int c4) { return n * kD + ((c4 ^ (n & 7)) << 2); }
 
 // Thread (tx, ty) = (tid % 16, tid / 16) holds rows MI ty .. and, of the
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_simt_kernel(const Paged
         for (int i = tid; i < R * 32; i += kSimtThreads) {
             const int r = i >> 5, c4 = i & 31;
             const int gr = w.p.qt * R + r, tok = a.group.quot(gr), g = gr - tok * a.group.d;
-            cp_async_16_or_0(smem_addr(qs + r * kD + 4 * c4),
+            cp_async_16_or_0(smem_addr(qs + r * kD + 4 * (c4 ^ (r / MI & 7))),
                              static_cast<const float *>(a.q) +
                                  (r < rows ? (int64_t)(w.s.row0 + tok) * a.q_st + (int64_t)(w.p.h * a.group.d + g) * a.q_sh + 4 * c4 : 0),
                              r < rows);
@@ -123,14 +124,14 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_simt_kernel(const Paged
             for (int i = 0; i < MI; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) z2[i][j] = 0;
-#pragma unroll 4
+#pragma unroll 2
             for (int c4 = 0; c4 < 32; ++c4) {
                 ulonglong2 kk[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) kk[j] = *reinterpret_cast<const ulonglong2 *>(ks + swz(tx + 16 * j, c4));
 #pragma unroll
                 for (int i = 0; i < MI; ++i) {
-                    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(qs + (MI * ty + i) * kD + 4 * c4);
+                    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(qs + (MI * ty + i) * kD + 4 * (c4 ^ (ty & 7)));
 #pragma unroll
                     for (int j = 0; j < 4; ++j) z2[i][j] = fma2(x.y, kk[j].y, fma2(x.x, kk[j].x, z2[i][j]));
                 }
@@ -173,7 +174,7 @@ __global__ void __launch_bounds__(kSimtThreads, 2) paged_simt_kernel(const Paged
             }
             asm volatile("cp.async.wait_group 1;" ::: "memory");  // this tile's values
             __syncthreads();
-#pragma unroll 4
+#pragma unroll 2
             for (int n = 0; n < BN; ++n) {
                 const ulonglong2 y0 = *reinterpret_cast<const ulonglong2 *>(vs + n * kD + 4 * tx);
                 const ulonglong2 y1 = *reinterpret_cast<const ulonglong2 *>(vs + n * kD + 64 + 4 * tx);

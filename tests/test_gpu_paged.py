@@ -383,3 +383,143 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for a, o in zip(args, want):
         assert torch.equal(a[6], o)
+
+
+# ------------------------------------------------------------- the calls together --
+
+def serve(cache, steps, Hq, Hkv, dtype, seed, freq, window):
+    """Run steps of new tokens through a PagedCache and check every call against plain fp64 on what the pages hold."""
+    g = torch.Generator().manual_seed(seed)
+    wq, wk = (1 + 0.2 * torch.randn((2, 128), generator=g)).to(dtype)
+    B = cache.B
+    lens, rows_seen = [0] * B, [[] for _ in range(B)]
+    for new in steps:
+        T = sum(new) + 3
+        qkv = torch.randn((T, Hq + 2 * Hkv, 128), generator=g).to(dtype)
+        dev = qkv.cuda()
+        q_out, out = (torch.full((T, Hq, 128), 9.0, dtype=dtype, device="cuda") for _ in range(2))
+        cache.extend(i32(new), rows=T)
+        cache.append(dev[:, :Hq], dev[:, Hq:Hq + Hkv], dev[:, Hq + Hkv:], q_out, wq.cuda(), wk.cuda(), 1e-6, freq, layer=1)
+        cache.attend(q_out, out, window=window, max_new=max(new), layer=1)
+        lens = [a + n for a, n in zip(lens, new)]
+        assert cache.kv_lens.tolist() == lens
+        q_start = [0]
+        for n in new:
+            q_start.append(q_start[-1] + n)
+        # keys and values where the tables say, at their positions
+        table, k_cache, v_cache = cache.block_table.tolist(), cache.k_cache[1].cpu(), cache.v_cache[1].cpu()
+        for b, n in enumerate(new):
+            pos = torch.arange(lens[b] - n, lens[b])
+            yk, sk = P.turned(qkv[q_start[b]:q_start[b + 1], Hq:Hq + Hkv], wk, 1e-6, freq.cpu(), False, pos)
+            for i, p in enumerate(pos.tolist()):
+                page, row = table[b][p // cache.page_size], p % cache.page_size
+                assert torch.equal(v_cache[page, :, row], qkv[q_start[b] + i, Hq + Hkv:])
+                err = (k_cache[page, :, row].to(P.F64) - yk[i]).abs()
+                assert (err <= 90 * 2.0 ** -24 * sk[i] + P.HALF_STEP[dtype] * (1 + 2.0 ** -6) * yk[i].abs() + 1e-30).all()
+        want, size, logit = P.attend(q_out[:T - 3].cpu(), k_cache, v_cache, table, q_start, lens, window, SCALE)
+        got = out.cpu().to(P.F64)
+        assert (got[T - 3:] == 9.0).all()
+        assert ((got[:T - 3] - want).abs() <= P.attend_bound(want, size, logit, dtype, max(lens + [1]))).all()
+        for b in range(B):
+            rows_seen[b].append(q_out[q_start[b]:q_start[b + 1]].cpu())
+    assert qdk.think_read_device_status(cache.extend_ws) == 0 and qdk.think_read_device_status(cache.attn_ws) == 0
+    return lens, rows_seen
+
+
+@pytest.mark.parametrize("dtype,window", [(BF, 0), (F32, 0), (BF, 100)])
+def test_prompts_then_decode_then_prune(dtype, window):
+    """Prompt chunks and single tokens of three requests through the pages; one is released and its pages serve a new
+    request; one is handed to the channel pruning and decoded from the thinner cache."""
+    import numpy as np
+    import oracle
+    Hq, Hkv, page = 8, 2, 32
+    cache = qdk.PagedCache(3, Hq, Hkv, num_pages=40, page_size=page, max_blocks=16, max_rows=512, layers=2, dtype=dtype)
+    freq = (10000.0 ** (-torch.arange(0, 128, 2, dtype=torch.float64) / 128)).cuda()
+    lens, rows = serve(cache, [[200, 0, 31], [97, 1, 1], [1, 130, 1], [1, 1, 1]], Hq, Hkv, dtype, 3, freq, window)
+    assert lens == [299, 132, 34] and cache.free_count.item() == 40 - 10 - 5 - 2
+    N, T = lens[0], 77
+    q_win = rows[0][1][-32:].transpose(0, 1)[None].contiguous()  # the last 32 queries of its second chunk
+    pruned, v = cache.prune(0, N, q_win.cuda(), T, layer=1)
+    k, _ = cache.gather(0, N, layer=1)
+    f64 = lambda t: t.cpu().to(torch.float64).numpy()
+    scores, idx, kp = oracle.oracle_prune(f64(q_win), f64(k), T)
+    from helpers import check_out, idx_mismatch_heads, kp_logical
+    assert not idx_mismatch_heads(pruned.idx.cpu().numpy(), idx, scores, T)
+    assert np.array_equal(kp_logical(pruned.k_pruned, N), kp)
+    q = torch.randn((1, Hq, 128), generator=torch.Generator().manual_seed(1)).to(dtype)
+    out = torch.empty((1, Hq, 128), dtype=torch.float32, device="cuda")
+    pruned.decode(q.cuda(), v, out)
+    check_out(out, oracle.oracle_decode(f64(q), kp, f64(v), idx), dtype)
+    cache.release(0)
+    assert cache.free_count.item() == 33 and cache.kv_lens.tolist() == [0, 132, 34]
+    held = [p for b in (1, 2) for p in cache.block_table[b].tolist() if p >= 0]
+    assert sorted(held + cache.free_pages[:33].tolist()) == list(range(40))
+
+
+def test_step_captured_and_replayed():
+    """Tables, write and attention of a decode step in one graph: replays advance the requests."""
+    Hq, Hkv, page, B = 8, 2, 16, 4
+    def fresh():
+        cache = qdk.PagedCache(B, Hq, Hkv, num_pages=64, page_size=page, max_blocks=16, max_rows=B)
+        return cache, torch.zeros((B, Hq, 128), dtype=BF, device="cuda"), torch.zeros((B, Hq, 128), dtype=BF, device="cuda")
+    freq = (10000.0 ** (-torch.arange(0, 128, 2, dtype=torch.float64) / 128)).cuda()
+    one = i32([1] * B)
+    qkv = torch.zeros((B, Hq + 2 * Hkv, 128), dtype=BF, device="cuda")
+
+    def step(c, q_out, out):
+        c.extend(one)
+        c.append(qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], q_out, inv_freq=freq)
+        c.attend(q_out, out, max_new=1)
+
+    inputs = [torch.randn(qkv.shape, generator=torch.Generator().manual_seed(i)).to(BF).cuda() for i in range(40)]
+    a, b = fresh(), fresh()
+    want = []
+    for x in inputs:
+        qkv.copy_(x)
+        step(*a)
+        want.append(a[2].clone())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(*b)
+    for x, w in zip(inputs, want):
+        qkv.copy_(x)
+        graph.replay()
+        assert torch.equal(b[2], w)
+    assert b[0].kv_lens.tolist() == [40] * B and torch.equal(a[0].block_table, b[0].block_table)
+
+
+@pytest.mark.parametrize("what", ["extend", "rope", "attn", "gather"])
+def test_binding_refusals_on_the_gpu(what):
+    """Shapes and types that do not match are refused before any launch."""
+    i = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    l = lambda *s: torch.zeros(s, dtype=torch.int64, device="cuda")
+    h = lambda *s: torch.zeros(s, dtype=BF, device="cuda")
+    w = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
+    if what == "extend":
+        good = [i(3), i(3), i(3, 4), i(9), i(1), 16, i(3), i(1), i(4), i(5), l(5), w]
+        bad = {0: i(4), 1: l(3), 2: i(4, 4), 3: i(3, 3), 4: i(2), 5: "x", 6: i(2), 7: i(0), 8: i(3), 9: l(5), 10: i(5),
+               11: w[::2]}
+        call = qdk.think_extend_pages
+    elif what == "rope":
+        good = [h(5, 4, 128), h(5, 2, 128), h(5, 2, 128), h(128), h(128), 1e-6, torch.zeros(64, dtype=torch.float64, device="cuda"),
+                False, i(5), l(5), h(5, 4, 128), h(3, 2, 16, 128), h(3, 2, 16, 128)]
+        bad = {0: h(5, 4, 128).float(), 1: h(4, 2, 128), 2: h(5, 3, 128), 3: h(64), 4: h(128).float(), 5: "x",
+               6: torch.zeros(64, device="cuda"), 7: torch.zeros(2), 8: l(5), 9: i(5), 10: h(5, 4, 64), 11: h(3, 1, 16, 128), 12: h(3, 2, 16, 128)[:2]}
+        call = qdk.think_norm_rope_append
+    elif what == "attn":
+        good = [h(5, 4, 128), h(3, 2, 16, 128), h(3, 2, 16, 128), i(2, 4), i(3), i(2), h(5, 4, 128),
+                torch.zeros(qdk.think_paged_attn_workspace_size(5, 4, 2), dtype=torch.uint8, device="cuda")]
+        bad = {0: h(5, 4, 128).float(), 1: h(3, 2, 16, 64), 2: h(2, 2, 16, 128), 3: l(2, 4), 4: i(2), 5: i(4)[::2],
+               6: h(4, 4, 128), 7: torch.zeros(256, dtype=torch.uint8, device="cuda")}
+        call = qdk.think_paged_attn
+    else:
+        good = [h(3, 2, 16, 128), i(2, 4), i(2), h(2, 2, 9, 128)]
+        bad = {0: h(3, 2, 16, 128).float(), 1: i(3, 4), 2: l(2), 3: h(2, 2, 9, 256)[..., ::2]}
+        call = qdk.think_gather_pages
+    call(*good)
+    for at, x in bad.items():
+        args = list(good)
+        args[at] = x
+        with pytest.raises(qdk.ThinkError):
+            call(*args)
