@@ -10,8 +10,8 @@
 
 #include "host.cuh"
 #include "paged_plan.cuh"
-#include "paged_simt.cuh"
 #include "paged_tc.cuh"
+#include "paged_tc32.cuh"
 #include "pages.cuh"
 #include "rope.cuh"
 #include "think.h"
@@ -46,44 +46,23 @@ think_status_t check_table(const int32_t *table, int64_t table_ld, int max_block
 }
 
 struct PagedPlan {
-    int rows;      // query rows of an item
-    int parts;     // blocks
     int sides;     // partials of a piece
-    int rows_cap;  // rows of a partial
-    size_t smem, ws_bytes;
+    int rows_cap;  // rows of a partial, a multiple of 4
+    size_t ws_bytes;
 };
 
-// bf16: items of 256 query rows, a block an SM.  fp32: items of 64 query rows,
-// two blocks an SM, or of 16 where no request has more rows than that.
-PagedPlan plan_paged(think_dtype_t dtype, int64_t T, int G, int max_new)
+// A block an SM; bf16: items of 256 query rows in two halves, fp32: of 128.
+PagedPlan plan_paged(think_dtype_t dtype, int64_t T, int G)
 {
     PagedPlan p;
-    if (dtype == THINK_BF16) {
-        p.rows = kPtRows;
-        p.parts = kTargetSMs;
-        p.sides = 2;
-        p.smem = paged_tc_smem();
-    } else {
-        p.rows = (int64_t)max_new * G <= 16 ? 16 : 64;
-        p.parts = kTargetSMs * 2;
-        p.sides = 1;
-        p.smem = p.rows == 16 ? paged_simt_smem<16>() : paged_simt_smem<64>();
-    }
-    // (the same for 16 and 64 rows, so that max_new does not change the workspace)
-    p.rows_cap = (int)std::min<int64_t>(dtype == THINK_BF16 ? 128 : 64, T * G);
-    static_assert(kPagedTickets >= 2 * kTargetSMs * sizeof(unsigned), "a counter a part");
-    p.ws_bytes = kPagedHeader + kPagedTickets + sizeof(float) * (size_t)p.parts * 2 * p.sides * (size_t)p.rows_cap * kPartLd;
+    p.sides = dtype == THINK_BF16 ? 2 : 1;
+    p.rows_cap = (int)std::min<int64_t>(128, ceil_div(T * G, 4) * 4);
+    static_assert(kPagedTickets >= kTargetSMs * sizeof(unsigned), "a counter a part");
+    p.ws_bytes = kPagedHeader + kPagedTickets + sizeof(float) * (size_t)kTargetSMs * 2 * p.sides * (size_t)p.rows_cap * kPartLd;
     return p;
 }
 
-template <int R>
-think_status_t launch_paged_simt(const PagedArgs &a, const PagedPlan &p, cudaStream_t st)
-{
-    if (!ensure_smem(reinterpret_cast<const void *>(&paged_simt_kernel<R>), p.smem)) return THINK_ERR_CUDA;
-    return launch_pdl(paged_simt_kernel<R>, dim3((unsigned)p.parts), dim3(kSimtThreads), p.smem, st, a);
-}
-
-think_status_t launch_paged_tc(const PagedArgs &a, const PagedPlan &p, cudaStream_t st)
+think_status_t launch_paged_tc(const PagedArgs &a, cudaStream_t st)
 {
     // rows of one TMA load: the largest power of two that divides the page, at most a tile
     const int chunk = std::min(kPtBN, a.page.d & -a.page.d);
@@ -91,8 +70,14 @@ think_status_t launch_paged_tc(const PagedArgs &a, const PagedPlan &p, cudaStrea
     if (!make_map_4d(&mk, THINK_BF16, a.k, kD, a.page.d, a.Hkv, a.num_pages, a.k_sn, a.k_sh, a.k_sp, 64, chunk, true) ||
         !make_map_4d(&mv, THINK_BF16, a.v, kD, a.page.d, a.Hkv, a.num_pages, a.v_sn, a.v_sh, a.v_sp, 64, chunk, true))
         return THINK_ERR_CUDA;
-    if (!ensure_smem(reinterpret_cast<const void *>(&paged_tc_kernel), p.smem)) return THINK_ERR_CUDA;
-    return launch_pdl(paged_tc_kernel, dim3((unsigned)p.parts), dim3(kPtThreads), p.smem, st, mk, mv, a, chunk);
+    if (!ensure_smem(reinterpret_cast<const void *>(&paged_tc_kernel), paged_tc_smem())) return THINK_ERR_CUDA;
+    return launch_pdl(paged_tc_kernel, dim3(kTargetSMs), dim3(kPtThreads), paged_tc_smem(), st, mk, mv, a, chunk);
+}
+
+think_status_t launch_paged_tc32(const PagedArgs &a, cudaStream_t st)
+{
+    if (!ensure_smem(reinterpret_cast<const void *>(&paged_tc32_kernel), kP32Smem)) return THINK_ERR_CUDA;
+    return launch_pdl(paged_tc32_kernel, dim3(kTargetSMs), dim3(kP32Threads), kP32Smem, st, a);
 }
 
 template <typename T, bool NEIGHBOURS>
@@ -222,7 +207,7 @@ think_status_t think_norm_rope_append(const void *q, const int64_t q_strides[2],
 size_t think_paged_attn_workspace_size(int64_t T, int Hq, int Hkv, int d, think_dtype_t dtype)
 {
     if (T < 0 || Hkv <= 0 || Hq < Hkv || Hq % Hkv != 0 || d != kD || !dtype_ok(dtype)) return 0;
-    return plan_paged(dtype, T, Hq / Hkv, 1).ws_bytes;
+    return plan_paged(dtype, T, Hq / Hkv).ws_bytes;
 }
 
 think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const void *k_cache,
@@ -253,7 +238,7 @@ think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const
             if (c[i] == 0 && (i == 0 ? num_pages : i == 1 ? Hkv : page_size) > 1) return THINK_ERR_INVALID_ARG;
             if (c[i] >= ((int64_t)1 << 40) / (int64_t)es) return THINK_ERR_UNSUPPORTED;
         }
-    const PagedPlan p = plan_paged(dtype, T, G, max_new > 0 ? (int)std::min<int64_t>(max_new, T) : (int)T);
+    const PagedPlan p = plan_paged(dtype, T, G);
     if (workspace_bytes < p.ws_bytes) return THINK_ERR_WORKSPACE;
     PagedArgs a = {};
     a.q = q, a.k = k_cache, a.v = v_cache, a.out = out;
@@ -268,11 +253,10 @@ think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const
     a.table_ld = table_ld;
     a.B = B, a.T = (int)T, a.Hkv = Hkv, a.group = Divisor(G), a.page = Divisor(page_size);
     a.num_pages = num_pages, a.limit = max_blocks * page_size, a.window = window;
-    a.rows_cap = p.rows_cap, a.parts = p.parts, a.sides = p.sides;
+    a.rows_cap = p.rows_cap, a.parts = kTargetSMs, a.sides = p.sides;
     a.scale_log2 = scale * 1.44269504088896341f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (dtype == THINK_BF16) return launch_paged_tc(a, p, st);
-    return p.rows == 16 ? launch_paged_simt<16>(a, p, st) : launch_paged_simt<64>(a, p, st);
+    return dtype == THINK_BF16 ? launch_paged_tc(a, st) : launch_paged_tc32(a, st);
 }
 
 think_status_t think_gather_pages(const void *cache, const int64_t cache_strides[3], int num_pages, int page_size,

@@ -327,36 +327,39 @@ __device__ __forceinline__ float *part_at(const PagedArgs &a, int part, int piec
 template <int N>
 __device__ __forceinline__ void store_out(float *p, const float (&x)[N])
 {
+    if constexpr (N % 4 == 0) {
 #pragma unroll
-    for (int i = 0; i < N; i += 2) *reinterpret_cast<float2 *>(p + i) = make_float2(x[i], x[i + 1]);
+        for (int i = 0; i < N; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = x[i];
+    }
 }
 template <int N>
 __device__ __forceinline__ void store_out(__nv_bfloat16 *p, const float (&x)[N])
 {
-    uint32_t w[N / 2];
+    if constexpr (N == 4) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+        *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    } else {
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        for (int i = 0; i < N; ++i) p[i] = __float2bfloat16_rn(x[i]);
     }
-    if constexpr (N == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    else *reinterpret_cast<uint32_t *>(p) = w[0];
 }
 
 // Join the pieces of an item, in the parts c0 .. c1:
 //     m = max m_i,  l = sum l_i 2^(m_i - m),  out = sum O_i 2^(m_i - m) / l.
-// A row that sees no key has l = 0 and gets zeros.  First m and l, with as many
-// lanes a row as 256 threads allow (a decode step has few rows and up to
-// hundreds of partials each), then eight channels of a row a thread (two with few
-// rows, so that more threads share the partials).  Rows are
-// the partials' fast dimension, so that neighbouring threads read neighbouring
-// words, and no load waits for another one.  The order of the sums is fixed, so
-// that the result does not depend on timing.  Called by 256 threads with sync()
-// as their barrier.
-constexpr int kMergeThreads = 256;
+// A row that sees no key has l = 0 and gets zeros.  First m, l and the factors
+// of the partials, with as many lanes a row as the threads allow (a decode step
+// has few rows and up to hundreds of partials each), then four rows of four
+// channels a thread (of one with few rows, so that more threads share them):
+// rows are the partials' fast dimension, a thread's loads are 16 bytes, and none
+// waits for another one.  Bound by the bytes that one block has in flight.  The
+// order of the sums is fixed, so that the result does not depend on timing.
+// Called by NT threads with sync() as their barrier.
 struct MergeSmem {
-    float m[kMergeThreads], inv[kMergeThreads];  // of a row: maximum, 1 / sum
-    float g[1024];                               // of a partial and row, where they fit: 2^(m_i - m) / l
+    float m[256], inv[256];  // of a row: maximum, 1 / sum
+    float4 g[1024];          // of a partial and four rows, where they fit: 2^(m_i - m) / l
 };
 // The parts c0 .. c1 that hold pieces of an item; whether all others are done.
 struct Pieces {
@@ -371,16 +374,17 @@ __device__ __forceinline__ void find_pieces(Pieces &x, const Parts &parts, const
     x.c1 = parts.of(tile0 + (w.t.j1 - w.t.j0) - 1);
 }
 
-template <typename T, int R, bool TWO_SIDES, typename Sync>
+
+template <typename T, int R, bool TWO_SIDES, int NT, typename Sync>
 __device__ __forceinline__ void merge_pieces(const PagedArgs &a, MergeSmem &sm, const Pieces &x, const Request &s, const Place &p,
                                              int tid, Sync sync)
 {
-    static_assert(R <= kMergeThreads, "a thread a row at least");
+    static_assert(R <= NT && R <= 256, "a thread a row at least");
     const int c0 = x.c0, c1 = x.c1;
-    const int rows = min(R, s.n * a.group.d - p.qt * R);
+    const int rows = min(R, s.n * a.group.d - p.qt * R), quads = (rows + 3) / 4;
     const bool two_sides = TWO_SIDES && rows <= R / 2;  // the two sides hold the same rows
     const int count = (c1 - c0 + 1) * (two_sides ? 2 : 1);
-    // element x of partial i of row r
+    // partial i from row r on
     auto at = [&](int i, int r) {
         const int part = c0 + (two_sides ? i >> 1 : i);
         const int side = two_sides ? i & 1 : TWO_SIDES ? r / (R / 2) : 0;
@@ -388,22 +392,25 @@ __device__ __forceinline__ void merge_pieces(const PagedArgs &a, MergeSmem &sm, 
     };
     const int64_t ld = a.rows_cap;
     int lanes = 32;  // of a row
-    while (rows * lanes > kMergeThreads) lanes >>= 1;
-    const bool kept = count <= 4 * lanes && count * rows <= 1024;
+    while (rows * lanes > NT) lanes >>= 1;
+    const bool kept = count * quads <= 1024;
     {
         const int r = tid / lanes, i0 = tid % lanes;
-        float m = -INFINITY, l = 0.f, mi[4], li[4];
-        for (int ib = i0; ib < count; ib += 4 * lanes) {
+        float m = -INFINITY, l = 0.f;
+        for (int ib = i0; ib < count; ib += 8 * lanes) {
+            float mi[8], li[8], mn = m;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+            for (int u = 0; u < 8; ++u) {
                 const int i = ib + u * lanes;
                 mi[u] = -INFINITY, li[u] = 0.f;
                 if (i < count && r < rows) mi[u] = __ldcg(at(i, r) + kD * ld), li[u] = __ldcg(at(i, r) + (kD + 1) * ld);
             }
-            const float mn = fmaxf(fmaxf(fmaxf(mi[0], mi[1]), fmaxf(mi[2], mi[3])), m), ref = mn == -INFINITY ? 0.f : mn;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) mn = fmaxf(mn, mi[u]);
+            const float ref = mn == -INFINITY ? 0.f : mn;
             l *= exp2f(m - ref);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) l += li[u] * exp2f(mi[u] - ref);
+            for (int u = 0; u < 8; ++u) l += li[u] * exp2f(mi[u] - ref);
             m = mn;
         }
         float top = m;
@@ -415,42 +422,60 @@ __device__ __forceinline__ void merge_pieces(const PagedArgs &a, MergeSmem &sm, 
         if (r < rows) {
             if (i0 == 0) sm.m[r] = ref, sm.inv[r] = inv;
             if (kept) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    if (i0 + u * lanes < count) sm.g[(i0 + u * lanes) * rows + r] = exp2f(mi[u] - ref) * inv;
+#pragma unroll 8
+                for (int i = i0; i < count; i += lanes)
+                    reinterpret_cast<float *>(&sm.g[i * quads + r / 4])[r & 3] = exp2f(__ldcg(at(i, r) + kD * ld) - ref) * inv;
             }
         }
     }
     sync();
     auto channels = [&](auto width) {
         constexpr int N = decltype(width)::value;
-        for (int k = tid; k < rows * (kD / N); k += kMergeThreads) {
-            const int c = k / rows * N, r = k % rows;
-            const float m = sm.m[r], inv = sm.inv[r];
-            float o[N];
+        for (int k = tid; k < quads * (kD / N); k += NT) {
+            const int c = k / quads * N, q = k % quads;
+            float4 o[N];
 #pragma unroll
-            for (int j = 0; j < N; ++j) o[j] = 0.f;
-#pragma unroll(32 / N)
+            for (int j = 0; j < N; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll(N == 1 ? 8 : 4)
             for (int i = 0; i < count; ++i) {
-                const float *x = at(i, r);
-                const float g = kept ? sm.g[i * rows + r] : exp2f(__ldcg(x + kD * ld) - m) * inv;
+                const float *y = at(i, 4 * q);
+                float4 g;
+                if (kept) {
+                    g = sm.g[i * quads + q];
+                } else {
+                    const float4 mi = __ldcg(reinterpret_cast<const float4 *>(y + kD * ld));
+                    const float4 m = *reinterpret_cast<const float4 *>(sm.m + 4 * q), inv = *reinterpret_cast<const float4 *>(sm.inv + 4 * q);
+                    g = make_float4(exp2f(mi.x - m.x) * inv.x, exp2f(mi.y - m.y) * inv.y, exp2f(mi.z - m.z) * inv.z,
+                                    exp2f(mi.w - m.w) * inv.w);
+                }
 #pragma unroll
-                for (int j = 0; j < N; ++j) o[j] += __ldcg(x + (c + j) * ld) * g;
+                for (int j = 0; j < N; ++j) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(y + (c + j) * ld));
+                    o[j].x += v.x * g.x, o[j].y += v.y * g.y, o[j].z += v.z * g.z, o[j].w += v.w * g.w;
+                }
             }
-            const int gr = p.qt * R + r, tok = a.group.quot(gr), g = gr - tok * a.group.d;
-            store_out(static_cast<T *>(a.out) + (int64_t)(s.row0 + tok) * a.o_st + (int64_t)(p.h * a.group.d + g) * a.o_sh + c, o);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = 4 * q + e, gr = p.qt * R + r;
+                if (r >= rows) break;
+                const int tok = a.group.quot(gr), g = gr - tok * a.group.d;
+                float z[N];
+#pragma unroll
+                for (int j = 0; j < N; ++j) z[j] = e == 0 ? o[j].x : e == 1 ? o[j].y : e == 2 ? o[j].z : o[j].w;
+                store_out(static_cast<T *>(a.out) + (int64_t)(s.row0 + tok) * a.o_st + (int64_t)(p.h * a.group.d + g) * a.o_sh + c, z);
+            }
         }
     };
-    if (rows > 4) channels(std::integral_constant<int, 8>{});
-    else channels(std::integral_constant<int, 2>{});
+    if (quads > 2) channels(std::integral_constant<int, 4>{});
+    else channels(std::integral_constant<int, 1>{});
 }
 
-// A piece's partial has been written by the calling 256 threads: count it, and
+// A piece's partial has been written by the calling NT threads: count it, and
 // join the item's pieces if it was the last one.  `x` (shared) comes from
 // find_pieces.  The counters are in the workspace, one a part (a part begins at
 // most one item that another one ends), and are zero again when the item is
 // done.
-template <typename T, int R, bool TWO_SIDES, typename W, typename Sync>
+template <typename T, int R, bool TWO_SIDES, int NT, typename W, typename Sync>
 __device__ __forceinline__ void finish_piece(const PagedArgs &a, MergeSmem &sm, Pieces &x, const W &w, int tid, Sync sync)
 {
     sync();
@@ -459,7 +484,7 @@ __device__ __forceinline__ void finish_piece(const PagedArgs &a, MergeSmem &sm, 
         if (x.last) a.tickets[x.c0] = 0u;
     }
     sync();
-    if (x.last) merge_pieces<T, R, TWO_SIDES>(a, sm, x, w.s, w.p, tid, sync);
+    if (x.last) merge_pieces<T, R, TWO_SIDES, NT>(a, sm, x, w.s, w.p, tid, sync);
     sync();
 }
 

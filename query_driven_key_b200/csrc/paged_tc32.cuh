@@ -1,0 +1,373 @@
+// paged_tc32.cuh -- attention of new tokens over the paged cache in fp32 on the
+// 5th-generation tensor cores (the plan: paged_plan.cuh).
+//
+// An fp32 number is the sum of three bf16 ones to its last bit or so: x = x0 +
+// x1 + x2, each the rounding of what the ones before it leave (8 significant
+// bits each).  A product of two such sums, without the terms below 2^-24 of
+// it, is
+//     x0 y2 + x2 y0 + x1 y1 + x0 y1 + x1 y0 + x0 y0,
+// six bf16 products with fp32 sums, added from the smallest on.  Both products
+// of the attention are formed that way, at a sixth of the bf16
+// rate, which is several times the rate of the FMA pipes:
+//     S = Q K^T      128 query rows x 64 keys; the parts of Q, K in shared memory
+//     P = 2^(s S - m) and its three parts: one thread a row, to TMEM
+//     O += P V       the parts of P in TMEM, those of V in shared memory
+// with the running reference m and sum l as in the bf16 kernel (m follows the
+// maximum when that has grown by more than 2^kPtLazy).
+//
+// Warps: 4 softmax (a thread a query row), 8 that bring keys, values and
+// queries (one row of 128 channels a warp at a time: loaded into registers a
+// tile ahead, split, and stored in the layouts of the products with the
+// 128-byte swizzle; rows that no query of the item sees are zeros, whatever
+// the page holds), 1 for the products.  Shared memory holds one tile of keys
+// and one of values (48 KB each with their parts) beside the queries (96 KB);
+// logits have two buffers in TMEM, so that the next tile's run beside this one's
+// softmax.  Bound by the products: 72 a tile, about 4100 cycles.
+// Every wait is bounded, as in the bf16 kernel.
+#pragma once
+
+#include "paged_tc.cuh"
+
+namespace think {
+
+constexpr int kP32Rows = 128;
+constexpr int kP32BN = 64;
+constexpr int kP32Softmax = 128;  // threads
+constexpr int kP32Bring = 256;
+constexpr int kP32Threads = kP32Softmax + kP32Bring + 32;
+constexpr int kP32Mma = (kP32Softmax + kP32Bring) / 32;
+constexpr uint32_t kP32QPart = 32768u;   // one part of Q: [2 channel halves][128 rows][128 B]
+constexpr uint32_t kP32KPart = 16384u;   // one part of a tile of K or V: [2][64][128 B]
+constexpr size_t kP32Smem = 1024u + 3u * kP32QPart + 6u * kP32KPart;
+
+struct P32Bars {
+    uint64_t q_full, q_empty, k_full, k_empty, v_full, p_full, pv_done, s_full[2], done;
+    uint32_t tmem;
+    uint32_t abort_flag;
+};
+
+// The three parts of two numbers, each as a pair of bf16.
+__device__ __forceinline__ void split3(float a, float b, uint32_t (&w)[3])
+{
+#pragma unroll
+    for (int p = 0; p < 3; ++p) {
+        w[p] = bf16_pair(a, b);
+        a -= bf16lo(w[p]);
+        b -= bf16hi(w[p]);
+    }
+}
+
+// The products' terms, smallest first: the parts of the left and of the right factor.
+__device__ __forceinline__ int term_left(int i) { return (0x021010 >> (4 * (5 - i))) & 15; }   // 0 2 1 0 1 0
+__device__ __forceinline__ int term_right(int i) { return (0x201100 >> (4 * (5 - i))) & 15; }  // 2 0 1 1 0 0
+
+__global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedArgs a)
+{
+    using W = Walk<kP32Rows, kP32BN>;
+    extern __shared__ unsigned char smem_dyn[];
+    unsigned char *qs = smem_dyn + ((1024u - (smem_addr(smem_dyn) & 1023u)) & 1023u);
+    unsigned char *ks = qs + 3 * kP32QPart, *vs = ks + 3 * kP32KPart;
+    __shared__ PlanSmem plan_sm;
+    __shared__ P32Bars bars;
+    __shared__ MergeSmem merge_sm;
+    __shared__ Pieces pieces;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile uint32_t *abort_flag = &bars.abort_flag;
+    const uint32_t q_full = smem_addr(&bars.q_full), q_empty = smem_addr(&bars.q_empty), k_full = smem_addr(&bars.k_full),
+                   k_empty = smem_addr(&bars.k_empty), v_full = smem_addr(&bars.v_full), p_full = smem_addr(&bars.p_full),
+                   pv_done = smem_addr(&bars.pv_done), s_full = smem_addr(bars.s_full), done = smem_addr(&bars.done);
+    if (tid == 0) {
+        mbar_init(q_full, kP32Bring / 32);
+        mbar_init(k_full, kP32Bring / 32);
+        mbar_init(v_full, kP32Bring / 32);
+        mbar_init(p_full, kP32Softmax / 32);
+        mbar_init(q_empty, 1);
+        mbar_init(k_empty, 1);
+        mbar_init(pv_done, 1);
+        mbar_init(s_full, 1);
+        mbar_init(s_full + 8, 1);
+        mbar_init(done, 1);
+        bars.abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == kP32Mma) {
+        tc05::tmem_alloc(smem_addr(&bars.tmem), 512);
+        tc05::tmem_relinquish();
+    }
+    grid_dependency_wait();
+    const int part = blockIdx.x;
+    const Parts parts = plan<kP32Rows, kP32BN, kP32Threads>(a, &plan_sm, part);
+    grid_launch_dependents();
+    tc05::fence_before_sync();
+    __syncthreads();
+    tc05::fence_after_sync();
+    const uint32_t tmem = bars.tmem;  // S 0 .. 127 (two buffers), O 128 .. 255, P 256 .. 351 (three parts)
+    const Place place = plan_sm.place;
+    bool ok = true;
+    auto wait = [&](uint32_t bar, uint32_t phase) {  // false from the first wait that runs out on
+        if (ok) ok = pt_wait(bar, phase & 1, abort_flag, a.status, THINK_DEVICE_TIMEOUT_FULL);
+        return ok;
+    };
+
+    if (warp == kP32Mma) {
+        // ------------------------------------------------------ the products
+        constexpr uint32_t idesc_s = tc05::idesc_bf16_f32<128, 64, false>();
+        constexpr uint32_t idesc_o = tc05::idesc_bf16_f32_bmn<128, 128>();
+        const bool leader = elect_one();
+        const uint64_t q_desc = tc05::smem_desc(smem_addr(qs), 16u, 1024u, tc05::kLayoutSwizzle128B);
+        const uint64_t k_desc = tc05::smem_desc(smem_addr(ks), 16u, 1024u, tc05::kLayoutSwizzle128B);
+        const uint64_t v_desc = tc05::smem_desc(smem_addr(vs), kP32KPart / 2, 1024u, tc05::kLayoutSwizzle128B);
+        uint32_t items = 0, nk = 0, nv = 0;  // items begun, key tiles and value tiles taken
+        for (W w(a, place, parts, part); w.live() && ok; w.next(), ++items) {
+            const int n = w.j1 - w.j0;
+            auto logits = [&](int j) {  // S = Q K_j^T
+                if (!wait(k_full, nk)) return;
+                tc05::fence_after_sync();
+                const uint32_t d = uniform(tmem + 64u * (nk & 1)), bar = uniform(s_full + 8 * (nk & 1));
+                ++nk;
+                if (leader) {
+#pragma unroll
+                    for (int i = 0; i < 6; ++i)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t oq = (uint32_t)term_left(i) * kP32QPart + (uint32_t)(k >> 2) * (kP32QPart / 2) + (k & 3) * 32u;
+                            const uint32_t ok_ = (uint32_t)term_right(i) * kP32KPart + (uint32_t)(k >> 2) * (kP32KPart / 2) + (k & 3) * 32u;
+                            tc05::mma_bf16(d, q_desc + (oq >> 4), k_desc + (ok_ >> 4), idesc_s, i > 0 || k > 0);
+                        }
+                    tc05::commit(bar);
+                    tc05::commit(k_empty);
+                    if (j + 1 == n) tc05::commit(q_empty);
+                }
+            };
+            wait(q_full, items);
+            logits(0);
+            for (int j = 0; j < n && ok; ++j) {
+                if (j + 1 < n) logits(j + 1);
+                wait(v_full, nv);
+                if (!wait(p_full, nv)) break;
+                ++nv;
+                tc05::fence_after_sync();
+                const bool more = uniform(j > 0) != 0;
+                if (leader) {  // O (+)= P V_j
+#pragma unroll
+                    for (int i = 0; i < 6; ++i)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc05::mma_bf16_ts(tmem + 128u, tmem + 256u + 32u * term_left(i) + 8u * k,
+                                              v_desc + (((uint32_t)term_right(i) * kP32KPart + 2048u * k) >> 4), idesc_o,
+                                              more || i > 0 || k > 0);
+                    tc05::commit(pv_done);
+                }
+            }
+        }
+        if (leader) {  // no product and no arrival may be under way when the block ends
+            tc05::commit(done);
+            mbar_wait_bounded(done, 0, a.status, THINK_DEVICE_TIMEOUT_FULL);
+        }
+        __syncwarp();
+    } else if (warp >= kP32Softmax / 32) {
+        // ------------------------------------------- keys, values and queries
+        const int bw = warp - kP32Softmax / 32;
+        const float flip = a.scale_log2 < 0.f ? -1.f : 1.f;  // a negative scale turns q
+        // channels 4 lane .. of a row go to 8 bytes of its line in half lane / 16
+        auto put = [&](unsigned char *base, uint32_t part_bytes, int row, uint4 v, float sign) {
+            uint32_t lo[3], hi[3];
+            split3(sign * __uint_as_float(v.x), sign * __uint_as_float(v.y), lo);
+            split3(sign * __uint_as_float(v.z), sign * __uint_as_float(v.w), hi);
+            unsigned char *p = base + (lane >> 4) * (part_bytes / 2) + row * 128 + ((((lane & 15) >> 1) ^ (row & 7)) << 4) + (lane & 1) * 8;
+#pragma unroll
+            for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2 *>(p + i * part_bytes) = make_uint2(lo[i], hi[i]);
+        };
+        auto hand_over = [&](uint32_t bar) {
+            tc05::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        const float *kp = static_cast<const float *>(a.k) + 4 * lane, *vp = static_cast<const float *>(a.v) + 4 * lane;
+        uint32_t items = 0, g = 0;  // items begun, tiles stored
+        for (W w(a, place, parts, part); w.live(); w.next(), ++items) {
+            // this warp's rows bw + 8 i of a tile: lane i looks row i up
+            int page = -1, row = 0;
+            auto locate = [&](int jt) {
+                const int key = jt * kP32BN + bw + 8 * (lane & 7);
+                page = -1, row = 0;
+                if (key >= w.t.lo && key < w.t.hi) {
+                    const int j = a.page.quot(key);
+                    page = a.table[(int64_t)w.p.b * a.table_ld + j];
+                    row = key - j * a.page.d;
+                    if ((unsigned)page >= (unsigned)a.num_pages) {
+                        page = -1;
+                        atomicOr(a.status, THINK_DEVICE_BAD_PAGE);
+                    }
+                }
+            };
+            uint4 kr[8], vr[8];
+            auto load = [&](const float *pool, int64_t sp, int64_t sh, int64_t sn, uint4 (&x)[8]) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int p = __shfl_sync(0xffffffffu, page, i), r = __shfl_sync(0xffffffffu, row, i);
+                    x[i] = load16(pool + (p >= 0 ? p * sp + w.p.h * sh + r * sn : 0), p >= 0);
+                }
+            };
+            locate(w.j0);
+            load(kp, a.k_sp, a.k_sh, a.k_sn, kr);
+            load(vp, a.v_sp, a.v_sh, a.v_sn, vr);
+            const int rows = min(kP32Rows, w.s.n * a.group.d - w.p.qt * kP32Rows);
+            if (items > 0) wait(q_empty, items - 1);
+            for (int r0 = bw; r0 < kP32Rows; r0 += 32) {  // four rows at a time
+                uint4 x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = r0 + 8 * i, gr = w.p.qt * kP32Rows + r, tok = a.group.quot(gr);
+                    x[i] = load16(static_cast<const float *>(a.q) + 4 * lane +
+                                      (r < rows ? (int64_t)(w.s.row0 + tok) * a.q_st +
+                                                      (int64_t)(w.p.h * a.group.d + gr - tok * a.group.d) * a.q_sh
+                                                : 0),
+                                  r < rows);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) put(qs, kP32QPart, r0 + 8 * i, x[i], flip);
+            }
+            hand_over(q_full);
+            for (int jt = w.j0; jt < w.j1; ++jt, ++g) {
+                const bool more = jt + 1 < w.j1;
+                if (g > 0) wait(k_empty, g - 1);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) put(ks, kP32KPart, bw + 8 * i, kr[i], 1.f);
+                hand_over(k_full);
+                if (more) {
+                    locate(jt + 1);
+                    load(kp, a.k_sp, a.k_sh, a.k_sn, kr);
+                }
+                if (g > 0) wait(pv_done, g - 1);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) put(vs, kP32KPart, bw + 8 * i, vr[i], 1.f);
+                hand_over(v_full);
+                if (more) load(vp, a.v_sp, a.v_sh, a.v_sn, vr);
+            }
+        }
+    } else {
+        // ----------------------------------------------------------- softmax
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * warp) << 16), o_addr = lane_addr + 128u, p_addr = lane_addr + 256u;
+        const float sl = fmaxf(fabsf(a.scale_log2), 1.0e-30f);  // a scale of 0 still sends -inf to -inf
+        uint32_t g = 0;  // tiles of the part
+        for (W w(a, place, parts, part); w.live(); w.next()) {
+            const int rows = min(kP32Rows, w.s.n * a.group.d - w.p.qt * kP32Rows);
+            const int row = w.p.qt * kP32Rows + tid, tok = a.group.quot(row);
+            const bool real = tid < rows;
+            const bool warp_real = __any_sync(0xffffffffu, real);
+            // (a row that is not real takes part as the last one of its request: what it holds is not stored)
+            const int pos = w.s.kv - w.s.n + (real ? tok : w.s.n - 1);
+            if (!w.whole && tid == 0) find_pieces(pieces, parts, w);
+            float m = -INFINITY, l = 0.f;
+            for (int jt = w.j0; jt < w.j1; ++jt, ++g) {
+                wait(s_full + 8 * (g & 1), g >> 1);
+                if (warp_real) {
+                    tc05::fence_after_sync();
+                    uint32_t u[2][32];
+                    tc05::tmem_ld32_issue(lane_addr + 64u * (g & 1), u[0]);
+                    tc05::tmem_ld32_issue(lane_addr + 64u * (g & 1) + 32u, u[1]);
+                    tc05::tmem_ld32_wait(u[0]);
+                    tc05::tmem_ld32_keep(u[1]);
+                    const int at = jt * kP32BN;
+                    const int chi = pos + 1 - at, clo = a.window > 0 ? pos - a.window + 1 - at : 0;
+                    if (!__all_sync(0xffffffffu, chi >= kP32BN && clo <= 0)) {
+#pragma unroll
+                        for (int c = 0; c < kP32BN; ++c)
+                            if (c >= chi || c < clo) u[c >> 5][c & 31] = 0xff800000u;  // -inf
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        mx[i] = __uint_as_float(u[i >> 1][16 * (i & 1)]);
+#pragma unroll
+                        for (int c = 1; c < 16; ++c) mx[i] = fmaxf(mx[i], __uint_as_float(u[i >> 1][16 * (i & 1) + c]));
+                    }
+                    const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const bool grow = (top - m) * sl > kPtLazy;  // NaN (both -inf): false
+                    const float f = grow ? exp2_approx((m - top) * sl) : 1.f;
+                    if (grow) m = top;
+                    l *= f;
+                    const float nm = m == -INFINITY ? 0.f : -m * sl;
+                    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < kP32BN; ++c) {
+                        const float p = exp2_approx(fmaf(__uint_as_float(u[c >> 5][c & 31]), sl, nm));
+                        s[c & 3] += p;
+                        u[c >> 5][c & 31] = __float_as_uint(p);
+                    }
+                    l += (s[0] + s[1]) + (s[2] + s[3]);
+                    if (g > 0) wait(pv_done, g - 1);  // P and O are free
+                    tc05::fence_after_sync();
+                    if (jt > w.j0 && __any_sync(0xffffffffu, grow)) {
+#pragma unroll 1
+                        for (int i = 0; i < 8; ++i) {
+                            uint32_t o[16];
+                            tc05::tmem_ld16_issue(o_addr + 16u * i, o);
+                            tc05::tmem_ld_wait(o);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                            tc05::tmem_st16(o_addr + 16u * i, o);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        uint32_t p[3][16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            uint32_t x[3];
+                            split3(__uint_as_float(u[i][2 * c]), __uint_as_float(u[i][2 * c + 1]), x);
+                            p[0][c] = x[0], p[1][c] = x[1], p[2][c] = x[2];
+                        }
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) tc05::tmem_st16(p_addr + 32u * k + 16u * i, p[k]);
+                    }
+                    tc05::tmem_st_wait();
+                    tc05::fence_before_sync();
+                } else if (g > 0) {
+                    wait(pv_done, g - 1);  // (each of its phases)
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full);
+            }
+            wait(pv_done, g - 1);
+            tc05::fence_after_sync();
+            if (warp_real) {
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                float *dst = static_cast<float *>(a.out) + (int64_t)(w.s.row0 + tok) * a.o_st +
+                             (int64_t)(w.p.h * a.group.d + row - tok * a.group.d) * a.o_sh;
+                float *pt = part_at(a, part, w.head ? 1 : 0, 0) + tid;  // element x of the row at pt[x * rows_cap]
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t o[32];
+                    tc05::tmem_ld32_issue(o_addr + 32u * i, o);
+                    tc05::tmem_ld32_wait(o);
+                    if (!real) continue;
+                    if (w.whole) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            *reinterpret_cast<float4 *>(dst + 32 * i + c) =
+                                make_float4(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 1]) * inv,
+                                            __uint_as_float(o[c + 2]) * inv, __uint_as_float(o[c + 3]) * inv);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) pt[(32 * i + c) * a.rows_cap] = __uint_as_float(o[c]);
+                    }
+                }
+                if (real && !w.whole) pt[kD * a.rows_cap] = m * sl, pt[(kD + 1) * a.rows_cap] = l;
+            }
+            tc05::fence_before_sync();
+            if (!w.whole)
+                finish_piece<float, kP32Rows, false, kP32Softmax>(a, merge_sm, pieces, w, tid, [] { named_barrier(1, kP32Softmax); });
+        }
+    }
+
+    tc05::fence_before_sync();
+    __syncthreads();
+    if (warp == kP32Mma) {
+        tc05::fence_after_sync();
+        tc05::tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace think
