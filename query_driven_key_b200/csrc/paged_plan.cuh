@@ -470,13 +470,14 @@ __device__ __forceinline__ void merge_pieces(const PagedArgs &a, MergeSmem &sm, 
     else channels(std::integral_constant<int, 1>{});
 }
 
-// A piece's partial has been written by the calling NT threads: count it, and
+// A piece's partial has been written by (some of) the calling NT threads: count it, and
 // join the item's pieces if it was the last one.  `x` (shared) comes from
 // find_pieces.  The counters are in the workspace, one a part (a part begins at
 // most one item that another one ends), and are zero again when the item is
 // done.
-template <typename T, int R, bool TWO_SIDES, int NT, typename W, typename Sync>
-__device__ __forceinline__ void finish_piece(const PagedArgs &a, MergeSmem &sm, Pieces &x, const W &w, int tid, Sync sync)
+template <typename T, int R, bool TWO_SIDES, int NT, typename Sync>
+__device__ __forceinline__ void finish_piece(const PagedArgs &a, MergeSmem &sm, Pieces &x, const Request &s, const Place &p,
+                                             int tid, Sync sync)
 {
     sync();
     if (tid == 0) {
@@ -484,7 +485,7 @@ __device__ __forceinline__ void finish_piece(const PagedArgs &a, MergeSmem &sm, 
         if (x.last) a.tickets[x.c0] = 0u;
     }
     sync();
-    if (x.last) merge_pieces<T, R, TWO_SIDES, NT>(a, sm, x, w.s, w.p, tid, sync);
+    if (x.last) merge_pieces<T, R, TWO_SIDES, NT>(a, sm, x, s, p, tid, sync);
     sync();
 }
 

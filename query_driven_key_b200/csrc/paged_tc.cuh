@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             tc05::fence_before_sync();
             if (!w.whole)
-                finish_piece<__nv_bfloat16, kPtRows, true, 256>(a, *reinterpret_cast<MergeSmem *>(qs + kPtTile), pieces, w, tid,
+                finish_piece<__nv_bfloat16, kPtRows, true, 256>(a, *reinterpret_cast<MergeSmem *>(qs + kPtTile), pieces, w.s, w.p, tid,
                                                            [] { named_barrier(2, 256); });
             if (late) load_q(nx);
             w.assign(nx);

@@ -109,6 +109,13 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
         return ok;
     };
 
+    // A part's last piece is counted, and its item joined, by the bringing
+    // warps too, which have nothing left to bring.
+    auto finish_last = [&](const Request &s, const Place &p) {
+        constexpr int NT = kP32Softmax + kP32Bring;
+        finish_piece<float, kP32Rows, false, NT>(a, merge_sm, pieces, s, p, tid, [] { named_barrier(2, NT); });
+    };
+
     if (warp == kP32Mma) {
         // ------------------------------------------------------ the products
         constexpr uint32_t idesc_s = tc05::idesc_bf16_f32<128, 64, false>();
@@ -185,7 +192,11 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
         };
         const float *kp = static_cast<const float *>(a.k) + 4 * lane, *vp = static_cast<const float *>(a.v) + 4 * lane;
         uint32_t items = 0, g = 0;  // items begun, tiles stored
+        bool cut = false;           // the part ends inside an item: this one
+        Request cut_s;
+        Place cut_p;
         for (W w(a, place, parts, part); w.live(); w.next(), ++items) {
+            cut = !w.whole, cut_s = w.s, cut_p = w.p;
             // this warp's rows bw + 8 i of a tile: lane i looks row i up
             int page = -1, row = 0;
             auto locate = [&](int jt) {
@@ -246,6 +257,7 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
                 if (more) load(vp, a.v_sp, a.v_sh, a.v_sn, vr);
             }
         }
+        if (cut) finish_last(cut_s, cut_p);
     } else {
         // ----------------------------------------------------------- softmax
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * warp) << 16), o_addr = lane_addr + 128u, p_addr = lane_addr + 256u;
@@ -357,8 +369,14 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
                 if (real && !w.whole) pt[kD * a.rows_cap] = m * sl, pt[(kD + 1) * a.rows_cap] = l;
             }
             tc05::fence_before_sync();
-            if (!w.whole)
-                finish_piece<float, kP32Rows, false, kP32Softmax>(a, merge_sm, pieces, w, tid, [] { named_barrier(1, kP32Softmax); });
+            if (!w.whole) {
+                W nx = w;
+                nx.next();
+                if (nx.live())
+                    finish_piece<float, kP32Rows, false, kP32Softmax>(a, merge_sm, pieces, w.s, w.p, tid,
+                                                                      [] { named_barrier(1, kP32Softmax); });
+                else finish_last(w.s, w.p);
+            }
         }
     }
 
