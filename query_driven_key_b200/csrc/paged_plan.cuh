@@ -131,10 +131,18 @@ struct Place {
     int b, h, qt, off;  // the item, and the units of it that lie before the place
 };
 
+// (Divisions of 64 bits take some hundred cycles, and every block starts with
+// three: most totals fit 32.)
+__device__ __forceinline__ int64_t quot64(int64_t x, int64_t d)  // x, d >= 0, d > 0
+{
+    return ((x | d) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)d) : x / d;
+}
+
 // Scratch of plan(): one block's.
 struct PlanSmem {
     int64_t ws[33];
     Place place;
+    Request request;  // of the place
 };
 
 // The sequence of `total` units in min(parts, total) parts, none of which is empty.
@@ -144,7 +152,7 @@ struct Parts {
     __device__ __forceinline__ Parts(int64_t units, int parts) : total(units)
     {
         n = (int)min((int64_t)parts, total);
-        per = n > 0 ? total / n : 0;
+        per = n > 0 ? quot64(total, n) : 0;
         rem = (int)(total - per * n);
     }
     // first unit of part i; total for the parts behind the last one
@@ -187,7 +195,7 @@ __device__ __forceinline__ Parts plan(const PagedArgs &a, PlanSmem *sm, int part
         if (rem >= 0 && rem < uh * a.Hkv) {  // this warp's request holds the place
             Place p;
             p.b = warp;
-            p.h = (int)(rem / uh);
+            p.h = (int)quot64(rem, uh);
             rem -= p.h * uh;
             const int nt = row_tiles<R>(a, s);
             for (int q0 = 0; q0 < nt; q0 += 32) {
@@ -201,6 +209,7 @@ __device__ __forceinline__ Parts plan(const PagedArgs &a, PlanSmem *sm, int part
                     p.qt = q0 + lane;
                     p.off = (int)rem - (end - n);
                     sm->place = p;
+                    sm->request = s;
                 }
                 rem -= __shfl_sync(0xffffffffu, end, 31);
                 if (rem < 0) break;
@@ -237,11 +246,11 @@ __device__ __forceinline__ Parts plan(const PagedArgs &a, PlanSmem *sm, int part
         x += base;
         if (u >= x - x0 && u < x) {  // this thread's request holds the place
             const Request s = load_request(a, b);
-            const int64_t uh = x0 / a.Hkv;
+            const int64_t uh = quot64(x0, a.Hkv);
             int64_t rem = u - (x - x0);
             Place p;
             p.b = b;
-            p.h = (int)(rem / uh);
+            p.h = (int)quot64(rem, uh);
             rem -= p.h * uh;
             for (p.qt = 0;; ++p.qt) {
                 const TileRange t = tile_range<R, BN>(a, s, p.qt);
@@ -250,6 +259,7 @@ __device__ __forceinline__ Parts plan(const PagedArgs &a, PlanSmem *sm, int part
             }
             p.off = (int)rem;
             sm->place = p;
+            sm->request = s;
         }
         base += chunk;
         __syncthreads();
@@ -269,12 +279,11 @@ struct Walk {
     TileRange t;    // the item
     int j0, j1;     // the piece
     bool whole, head;  // head: the piece begins with the item
-    __device__ __forceinline__ Walk(const PagedArgs &args, const Place &place, const Parts &parts, int part)
-        : a(args), p(place), first(parts.begin(part)), left(parts.begin(part + 1) - first)
+    __device__ __forceinline__ Walk(const PagedArgs &args, const PlanSmem &plan, const Parts &parts, int part)
+        : a(args), p(plan.place), s(plan.request), first(parts.begin(part)), left(parts.begin(part + 1) - first)
     {
         if (left > 0) {
             first -= p.off;
-            s = load_request(a, p.b);
             set();
         }
     }
@@ -393,12 +402,12 @@ __device__ __forceinline__ void merge_pieces(const PagedArgs &a, MergeSmem &sm, 
     const int64_t ld = a.rows_cap;
     int lanes = 32;  // of a row
     while (rows * lanes > NT) lanes >>= 1;
-    const bool kept = count * quads <= 1024;
+    const bool kept = count * quads <= 1024 && count <= 8 * lanes;
     {
         const int r = tid / lanes, i0 = tid % lanes;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, mi[8];
         for (int ib = i0; ib < count; ib += 8 * lanes) {
-            float mi[8], li[8], mn = m;
+            float li[8], mn = m;
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
                 const int i = ib + u * lanes;
@@ -422,9 +431,11 @@ __device__ __forceinline__ void merge_pieces(const PagedArgs &a, MergeSmem &sm, 
         if (r < rows) {
             if (i0 == 0) sm.m[r] = ref, sm.inv[r] = inv;
             if (kept) {
-#pragma unroll 8
-                for (int i = i0; i < count; i += lanes)
-                    reinterpret_cast<float *>(&sm.g[i * quads + r / 4])[r & 3] = exp2f(__ldcg(at(i, r) + kD * ld) - ref) * inv;
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int i = i0 + u * lanes;
+                    if (i < count) reinterpret_cast<float *>(&sm.g[i * quads + r / 4])[r & 3] = exp2f(mi[u] - ref) * inv;
+                }
             }
         }
     }

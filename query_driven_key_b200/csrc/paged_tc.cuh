@@ -225,7 +225,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     __syncthreads();
     tc05::fence_after_sync();
     const uint32_t tmem = bars.tmem;
-    const Place place = plan_sm.place;
 
     // A softmax thread holds a row of 128 logits: 384 x 168 registers at launch
     // = 256 x 216 for the softmax warps + 128 x 72 for the others.
@@ -241,7 +240,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         uint32_t ld = 0;                     // loads issued: stage ld % kPtStages
         uint32_t phases = 0, used = 0;       // of each full barrier its next phase; of each stage the last one's set
         bool ok = true;
-        for (W w(a, place, parts, part); w.live() && ok; w.next()) {
+        for (W w(a, plan_sm, parts, part); w.live() && ok; w.next()) {
             const PtItem x = pt_item(a, w);
             const PtOrder order{x.split ? 2 : 1, x.n};
             // this lane's rows of load i: the table entry (-1: no key of them is
@@ -310,7 +309,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const uint64_t v_desc = tc05::smem_desc(smem_addr(ring), 16384u, 1024u, tc05::kLayoutSwizzle128B);
         const uint32_t s_tmem = uniform(tmem + 128u * t), o_tmem = s_tmem + 256u;
         const uint32_t s_bar = uniform(sfull0 + 8 * t), o_bar = uniform(ofull0 + 8 * t);
-        for (W w(a, place, parts, part); w.live() && ok; w.next()) {
+        for (W w(a, plan_sm, parts, part); w.live() && ok; w.next()) {
             const PtItem x = pt_item(a, w);
             const PtOrder order{x.split ? 2 : 1, x.n};
             const int j0 = x.split ? t : 0, step = x.split ? 2 : 1;
@@ -450,7 +449,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(qfull0 + (x.split ? 16 : 8 * t));
         };
-        W w(a, place, parts, part);
+        W w(a, plan_sm, parts, part);
         if (w.live()) load_q(w);
         while (w.live()) {
             const PtItem x = pt_item(a, w);

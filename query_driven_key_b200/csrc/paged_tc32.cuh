@@ -102,7 +102,6 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
     __syncthreads();
     tc05::fence_after_sync();
     const uint32_t tmem = bars.tmem;  // S 0 .. 127 (two buffers), O 128 .. 255, P 256 .. 351 (three parts)
-    const Place place = plan_sm.place;
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t phase) {  // false from the first wait that runs out on
         if (ok) ok = pt_wait(bar, phase & 1, abort_flag, a.status, THINK_DEVICE_TIMEOUT_FULL);
@@ -125,7 +124,7 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
         const uint64_t k_desc = tc05::smem_desc(smem_addr(ks), 16u, 1024u, tc05::kLayoutSwizzle128B);
         const uint64_t v_desc = tc05::smem_desc(smem_addr(vs), kP32KPart / 2, 1024u, tc05::kLayoutSwizzle128B);
         uint32_t items = 0, nk = 0, nv = 0;  // items begun, key tiles and value tiles taken
-        for (W w(a, place, parts, part); w.live() && ok; w.next(), ++items) {
+        for (W w(a, plan_sm, parts, part); w.live() && ok; w.next(), ++items) {
             const int n = w.j1 - w.j0;
             auto logits = [&](int j) {  // S = Q K_j^T
                 if (!wait(k_full, nk)) return;
@@ -195,7 +194,7 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
         bool cut = false;           // the part ends inside an item: this one
         Request cut_s;
         Place cut_p;
-        for (W w(a, place, parts, part); w.live(); w.next(), ++items) {
+        for (W w(a, plan_sm, parts, part); w.live(); w.next(), ++items) {
             cut = !w.whole, cut_s = w.s, cut_p = w.p;
             // this warp's rows bw + 8 i of a tile: lane i looks row i up
             int page = -1, row = 0;
@@ -263,7 +262,7 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * warp) << 16), o_addr = lane_addr + 128u, p_addr = lane_addr + 256u;
         const float sl = fmaxf(fabsf(a.scale_log2), 1.0e-30f);  // a scale of 0 still sends -inf to -inf
         uint32_t g = 0;  // tiles of the part
-        for (W w(a, place, parts, part); w.live(); w.next()) {
+        for (W w(a, plan_sm, parts, part); w.live(); w.next()) {
             const int rows = min(kP32Rows, w.s.n * a.group.d - w.p.qt * kP32Rows);
             const int row = w.p.qt * kP32Rows + tid, tok = a.group.quot(row);
             const bool real = tid < rows;
