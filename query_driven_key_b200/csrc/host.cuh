@@ -114,24 +114,24 @@ EncodeTiledFn encode_fn()
 struct MapKey {
     const void *base;
     uint64_t dims[4], strides[3];
-    uint32_t box[2];
+    uint32_t box[3];
     int dtype, swizzle;
 };
 
 bool map_cache_find(const MapKey &k, CUtensorMap *m);
 void map_cache_put(const MapKey &k, const CUtensorMap &m);
 
-// 4-D map over (x, y, z, w) with element strides sy, sz, sw for y, z, w; box (bx, by, 1, 1).
+// 4-D map over (x, y, z, w) with element strides sy, sz, sw for y, z, w; box (bx, by, bz, 1).
 bool make_map_4d(CUtensorMap *m, think_dtype_t dt, const void *base, uint64_t dx, uint64_t dy,
                  uint64_t dz, uint64_t dw, int64_t sy, int64_t sz, int64_t sw, uint32_t bx,
-                 uint32_t by, bool swizzle128 = false)
+                 uint32_t by, bool swizzle128 = false, uint32_t bz = 1)
 {
     MapKey key;
     memset(&key, 0, sizeof(key));
     key.base = base;
     key.dims[0] = dx, key.dims[1] = dy, key.dims[2] = dz, key.dims[3] = dw;
     key.strides[0] = (uint64_t)sy, key.strides[1] = (uint64_t)sz, key.strides[2] = (uint64_t)sw;
-    key.box[0] = bx, key.box[1] = by;
+    key.box[0] = bx, key.box[1] = by, key.box[2] = bz;
     key.dtype = (int)dt;
     key.swizzle = swizzle128 ? 1 : 0;
     if (map_cache_find(key, m)) return true;
@@ -140,7 +140,7 @@ bool make_map_4d(CUtensorMap *m, think_dtype_t dt, const void *base, uint64_t dx
     const size_t es = esize(dt);
     cuuint64_t dims[4] = {dx, dy, dz, dw};
     cuuint64_t strides[3] = {(cuuint64_t)sy * es, (cuuint64_t)sz * es, (cuuint64_t)sw * es};
-    cuuint32_t box[4] = {bx, by, 1, 1};
+    cuuint32_t box[4] = {bx, by, bz, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     const CUresult r = fn(m, dt == THINK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,

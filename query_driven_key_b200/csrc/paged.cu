@@ -66,12 +66,22 @@ think_status_t launch_paged_tc(const PagedArgs &a, cudaStream_t st)
 {
     // rows of one TMA load: the largest power of two that divides the page, at most a tile
     const int chunk = std::min(kPtBN, a.page.d & -a.page.d);
-    CUtensorMap mk, mv;
+    // a tile's 128 query rows, tokens x heads of a group, as one TMA box; not if
+    // the group does not divide them, a negative scale turns them on the way, or
+    // the strides are none of TMA's
+    const int G = a.group.d, Hq = a.Hkv * G;
+    const auto fits = [](int64_t stride, int n) { return n == 1 || (stride > 0 && stride < ((int64_t)1 << 39)); };
+    const bool tma_q = 128 % G == 0 && a.scale_log2 >= 0.f && fits(a.q_sh, Hq) && fits(a.q_st, a.T);
+    CUtensorMap mk, mv, mq;
     if (!make_map_4d(&mk, THINK_BF16, a.k, kD, a.page.d, a.Hkv, a.num_pages, a.k_sn, a.k_sh, a.k_sp, 64, chunk, true) ||
         !make_map_4d(&mv, THINK_BF16, a.v, kD, a.page.d, a.Hkv, a.num_pages, a.v_sn, a.v_sh, a.v_sp, 64, chunk, true))
         return THINK_ERR_CUDA;
+    // (the stride of a dimension of one element is free)
+    if (!tma_q) mq = mk;
+    else if (!make_map_4d(&mq, THINK_BF16, a.q, kD, Hq, a.T, 1, Hq > 1 ? a.q_sh : kD, a.T > 1 ? a.q_st : kD, kD, 64, G, true, 128 / G))
+        return THINK_ERR_CUDA;
     if (!ensure_smem(reinterpret_cast<const void *>(&paged_tc_kernel), paged_tc_smem())) return THINK_ERR_CUDA;
-    return launch_pdl(paged_tc_kernel, dim3(kTargetSMs), dim3(kPtThreads), paged_tc_smem(), st, mk, mv, a, chunk);
+    return launch_pdl(paged_tc_kernel, dim3(kTargetSMs), dim3(kPtThreads), paged_tc_smem(), st, mk, mv, mq, a, chunk, tma_q);
 }
 
 think_status_t launch_paged_tc32(const PagedArgs &a, cudaStream_t st)

@@ -56,6 +56,7 @@ struct PtBars {
     uint64_t full[3][kPtStages];  // loads: for both, for warpgroup 0, for 1
     uint64_t empty[kPtStages];
     uint64_t q_full[3];  // Q of warpgroup 0, of 1, of a split item
+    uint64_t q_free[3];  // its place: of a warpgroup between items of split rows, of both around split items
     uint64_t s_full[2], o_full[2];
     uint64_t p_full[4];  // [t]: the early part of P, [2 + t]: all of it
     uint64_t turn[2];    // warpgroup t's products may go next
@@ -180,8 +181,8 @@ struct PtOrder {
 };
 
 __global__ void __launch_bounds__(kPtThreads, 1)
-    paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const PagedArgs a,
-                    const int chunk)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ CUtensorMap tm_q, const PagedArgs a, const int chunk, const bool tma_q)
 {
     using W = Walk<kPtRows, kPtBN>;
     extern __shared__ unsigned char smem_dyn[];
@@ -193,14 +194,16 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     unsigned char *qs = smem, *ring = smem + 2 * kPtTile;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile uint32_t *abort_flag = &bars.abort_flag;
-    const uint32_t full0 = smem_addr(bars.full), empty0 = smem_addr(bars.empty), qfull0 = smem_addr(bars.q_full),
+    const uint32_t full0 = smem_addr(bars.full), empty0 = smem_addr(bars.empty), qfull0 = smem_addr(bars.q_full), qfree0 = smem_addr(bars.q_free),
                    sfull0 = smem_addr(bars.s_full), pfull0 = smem_addr(bars.p_full), ofull0 = smem_addr(bars.o_full), turn0 = smem_addr(bars.turn), done = smem_addr(&bars.done);
     if (tid == 0) {
         for (int s = 0; s < 3 * kPtStages; ++s) mbar_init(full0 + 8 * s, 2);
         for (int s = 0; s < kPtStages; ++s) mbar_init(empty0 + 8 * s, 2);
-        mbar_init(qfull0 + 16, 8);
+        mbar_init(qfull0 + 16, tma_q ? 1 : 8);
+        mbar_init(qfree0 + 16, 8);
         for (int t = 0; t < 2; ++t) {
-            mbar_init(qfull0 + 8 * t, 4);
+            mbar_init(qfull0 + 8 * t, tma_q ? 1 : 4);
+            mbar_init(qfree0 + 8 * t, 4);
             mbar_init(sfull0 + 8 * t, 1);
             mbar_init(pfull0 + 8 * t, 4);
             mbar_init(pfull0 + 16 + 8 * t, 4);
@@ -212,6 +215,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         fence_barrier_init();
         prefetch_tensormap(&tm_k);
         prefetch_tensormap(&tm_v);
+        prefetch_tensormap(&tm_q);
     }
     if (warp == kPtMma) {
         tc05::tmem_alloc(smem_addr(&bars.tmem), 512);
@@ -298,6 +302,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int t = warp - kPtMma;
         const bool leader = elect_one();
         uint32_t base = 0;              // loads of the items before
+        uint32_t items = 0, nfree = 0, nfree2 = 0;
+        bool was_split = false;
         uint32_t nq = 0, nqs = 0, np = 0, nt = t ^ 1;  // items begun (rows split, keys split), P tiles taken, turns
         uint32_t phases = 0;               // of each full barrier of the two sets waited on
         bool ok = true;
@@ -345,8 +351,24 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             auto pass = [&]() {
                 if (leader) mbar_arrive(turn0 + 8 * (t ^ 1));
             };
-            if (x.split) wait(qfull0 + 16, nqs++, THINK_DEVICE_TIMEOUT_FULL);
-            else wait(qfull0 + 8 * t, nq++, THINK_DEVICE_TIMEOUT_FULL);
+            const uint32_t q_bar = qfull0 + (x.split ? 16 : 8 * t);
+            if (tma_q) {  // bring Q: each warp its own rows, the first one those of a split item
+                if (items > 0) {
+                    if (x.split || was_split) wait(qfree0 + 16, nfree2++, THINK_DEVICE_TIMEOUT_EMPTY);
+                    else wait(qfree0 + 8 * t, nfree++, THINK_DEVICE_TIMEOUT_EMPTY);
+                }
+                ++items;
+                was_split = x.split;
+                if (leader && ok && !(x.split && t)) {
+                    const int tok = w.s.row0 + a.group.quot(w.p.qt * kPtRows + (x.split ? 0 : 128 * t));
+                    const uint32_t dst = smem_addr(qs) + (x.split ? 0u : t * kPtTile);
+                    mbar_arrive_expect_tx(q_bar, kPtTile);
+                    tma_load_4d(dst, &tm_q, 0, w.p.h * a.group.d, tok, 0, q_bar);
+                    tma_load_4d(dst + 16384u, &tm_q, 64, w.p.h * a.group.d, tok, 0, q_bar);
+                }
+                __syncwarp();
+            }
+            wait(q_bar, x.split ? nqs++ : nq++, THINK_DEVICE_TIMEOUT_FULL);
             if (j0 < x.n) {
                 const uint32_t s = take(order.key(j0));
                 tc05::fence_after_sync();
@@ -396,7 +418,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             base += order.loads();
         }
-        // no product and no arrival may be under way when the block ends
+        // no load, product or arrival may be under way when the block ends
+        if (!ok && tma_q && !(was_split && t))
+            mbar_wait_bounded(qfull0 + (was_split ? 16 : 8 * t), ((was_split ? nqs : nq) - 1) & 1, a.status, THINK_DEVICE_TIMEOUT_FULL);
         if (leader) {
             tc05::commit(done);
             mbar_wait_bounded(done, 0, a.status, THINK_DEVICE_TIMEOUT_FULL);
@@ -413,12 +437,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const float sl = fmaxf(fabsf(a.scale_log2), 1.0e-30f);  // a scale of 0 still sends -inf to -inf
         const uint32_t flip = a.scale_log2 < 0.f ? 0x80008000u : 0u;  // a negative one turns q
         const uint64_t sl2 = pack2(sl, sl);
-        uint32_t ns = 0, no = 0;
+        uint32_t ns = 0, no = 0, nsplit = 0;
         bool was_split = false;
         auto wait = [&](uint32_t bar, uint32_t phase) {
             pt_wait(bar, phase & 1, abort_flag, a.status, THINK_DEVICE_TIMEOUT_FULL);
         };
-        // Q of an item: a warpgroup's own rows, the products of whose last tile
+        // Q of an item, where its rows do not make a TMA box (see the products'
+        // warps): a warpgroup's own rows, the products of whose last tile
         // have been waited for; in and around split items the rows are shared,
         // so that both warpgroups have to be there
         auto load_q = [&](const W &w) {
@@ -450,7 +475,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (lane == 0) mbar_arrive(qfull0 + (x.split ? 16 : 8 * t));
         };
         W w(a, plan_sm, parts, part);
-        if (w.live()) load_q(w);
+        if (w.live() && !tma_q) load_q(w);
         while (w.live()) {
             const PtItem x = pt_item(a, w);
             const int base = w.s.kv - w.s.n;
@@ -546,13 +571,27 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
             }
             const bool any = j0 < x.n;  // this warpgroup had key tiles
+            // (A warpgroup without any does not run ahead of the other one: the
+            // item's Q comes when both have let the one before go.)
+            if (tma_q && x.split) wait(qfull0 + 16, nsplit++);
             const bool join = x.split && w.whole && x.n > 1;
             // the next item's Q, unless it needs the second Q tile while that is
             // used below: its first products then run beside this item's end
             W nx = w;
             nx.next();
             const bool late = (join || !w.whole) && nx.live() && !pt_item(a, nx).split;
-            if (!late && nx.live()) load_q(nx);
+            // the next item's Q may come: (with TMA) say so, or bring it
+            auto next_q = [&]() {
+                if (!nx.live()) return;
+                if (!tma_q) {
+                    load_q(nx);
+                    return;
+                }
+                tc05::fence_proxy_async_smem();  // the scratch in the second Q tile
+                __syncwarp();
+                if (lane == 0) mbar_arrive(qfree0 + (x.split || pt_item(a, nx).split ? 16 : 8 * t));
+            };
+            if (!late) next_q();
             if (any) wait(ofull0 + 8 * t, no++);
             tc05::fence_after_sync();
             auto load_o = [&](int i, uint32_t (&o)[32]) {
@@ -636,7 +675,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (!w.whole)
                 finish_piece<__nv_bfloat16, kPtRows, true, 256>(a, *reinterpret_cast<MergeSmem *>(qs + kPtTile), pieces, w.s, w.p, tid,
                                                            [] { named_barrier(2, 256); });
-            if (late) load_q(nx);
+            if (late) next_q();
             w.assign(nx);
         }
     }

@@ -243,9 +243,9 @@ def test_attn_large_logits(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_attn_strides_and_views(dtype):
+@pytest.mark.parametrize("Hq,Hkv", [(6, 2), (8, 2)])
+def test_attn_strides_and_views(dtype, Hq, Hkv):
     """q a view of a fused projection, out a view of a wider buffer, the table a view: canaries around stay."""
-    Hq, Hkv = 6, 2
     x = P.Batch([33, 2], [100, 60], Hq, Hkv, 32, dtype, 8)
     wide = torch.full((x.T, Hq + 3, 192), 5.0, dtype=dtype, device="cuda")
     q = wide[:, 1:1 + Hq, 32:160]
@@ -259,6 +259,12 @@ def test_attn_strides_and_views(dtype):
     assert torch.equal(out, run_attn(x, Hq, Hkv))
     out.fill_(5.0)
     assert (dst == 5.0).all()
+    # one row of queries for all tokens and heads
+    x.q[:] = x.q[:1, :1].clone()
+    w = attn_ws(x.T, Hq, Hkv, dtype)
+    qdk.think_paged_attn(x.q[:1, :1].cuda().expand(x.T, Hq, 128), x.cache(x.k), x.cache(x.v), i32(x.table), i32(x.q_start),
+                         i32(x.lens), out, w)
+    assert torch.equal(out, run_attn(x, Hq, Hkv))
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
