@@ -15,8 +15,8 @@
 // with the running reference m and sum l as in the bf16 kernel (m follows the
 // maximum when that has grown by more than 2^kPtLazy).
 //
-// Warps: 4 softmax (a thread a query row), 8 that bring keys, values and
-// queries (one row of 128 channels a warp at a time: loaded into registers a
+// Warps: 4 softmax (a thread a query row), 4 that bring keys and 4 values, with
+// the queries (one row of 128 channels a warp at a time: loaded into registers a
 // tile ahead, split, and stored in the layouts of the products with the
 // 128-byte swizzle; rows that no query of the item sees are zeros, whatever
 // the page holds), 1 for the products.  Shared memory holds one tile of keys
@@ -78,8 +78,8 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
                    pv_done = smem_addr(&bars.pv_done), s_full = smem_addr(bars.s_full), done = smem_addr(&bars.done);
     if (tid == 0) {
         mbar_init(q_full, kP32Bring / 32);
-        mbar_init(k_full, kP32Bring / 32);
-        mbar_init(v_full, kP32Bring / 32);
+        mbar_init(k_full, kP32Bring / 64);
+        mbar_init(v_full, kP32Bring / 64);
         mbar_init(p_full, kP32Softmax / 32);
         mbar_init(q_empty, 1);
         mbar_init(k_empty, 1);
@@ -173,7 +173,10 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
         __syncwarp();
     } else if (warp >= kP32Softmax / 32) {
         // ------------------------------------------- keys, values and queries
+        // Warps 0 .. 3 bring keys, 4 .. 7 values, each at its own pace; queries
+        // all of them.
         const int bw = warp - kP32Softmax / 32;
+        const bool keys = bw < kP32Bring / 64;
         const float flip = a.scale_log2 < 0.f ? -1.f : 1.f;  // a negative scale turns q
         // channels 4 lane .. of a row go to 8 bytes of its line in half lane / 16
         auto put = [&](unsigned char *base, uint32_t part_bytes, int row, uint4 v, float sign) {
@@ -189,18 +192,21 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        const float *kp = static_cast<const float *>(a.k) + 4 * lane, *vp = static_cast<const float *>(a.v) + 4 * lane;
+        const float *pool = static_cast<const float *>(keys ? a.k : a.v) + 4 * lane;
+        const int64_t sp = keys ? a.k_sp : a.v_sp, sh = keys ? a.k_sh : a.v_sh, sn = keys ? a.k_sn : a.v_sn;
+        unsigned char *tile = keys ? ks : vs;
+        const uint32_t full = keys ? k_full : v_full, empty = keys ? k_empty : pv_done;
+        const int r0 = bw & 3;  // this warp's rows r0 + 4 i of a tile: lane i looks row i up
         uint32_t items = 0, g = 0;  // items begun, tiles stored
         bool cut = false;           // the part ends inside an item: this one
         Request cut_s;
         Place cut_p;
         for (W w(a, plan_sm, parts, part); w.live(); w.next(), ++items) {
             cut = !w.whole, cut_s = w.s, cut_p = w.p;
-            // this warp's rows bw + 8 i of a tile: lane i looks row i up
-            int page = -1, row = 0;
-            auto locate = [&](int jt) {
-                const int key = jt * kP32BN + bw + 8 * (lane & 7);
-                page = -1, row = 0;
+            uint4 x[16];
+            auto load = [&](int jt) {
+                const int key = jt * kP32BN + r0 + 4 * (lane & 15);
+                int page = -1, row = 0;
                 if (key >= w.t.lo && key < w.t.hi) {
                     const int j = a.page.quot(key);
                     page = a.table[(int64_t)w.p.b * a.table_ld + j];
@@ -210,50 +216,37 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
                         atomicOr(a.status, THINK_DEVICE_BAD_PAGE);
                     }
                 }
-            };
-            uint4 kr[8], vr[8];
-            auto load = [&](const float *pool, int64_t sp, int64_t sh, int64_t sn, uint4 (&x)[8]) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < 16; ++i) {
                     const int p = __shfl_sync(0xffffffffu, page, i), r = __shfl_sync(0xffffffffu, row, i);
                     x[i] = load16(pool + (p >= 0 ? p * sp + w.p.h * sh + r * sn : 0), p >= 0);
                 }
             };
-            locate(w.j0);
-            load(kp, a.k_sp, a.k_sh, a.k_sn, kr);
-            load(vp, a.v_sp, a.v_sh, a.v_sn, vr);
+            load(w.j0);
             const int rows = min(kP32Rows, w.s.n * a.group.d - w.p.qt * kP32Rows);
             if (items > 0) wait(q_empty, items - 1);
-            for (int r0 = bw; r0 < kP32Rows; r0 += 32) {  // four rows at a time
-                uint4 x[4];
+#pragma unroll 1
+            for (int q0 = bw; q0 < kP32Rows; q0 += 32) {  // four rows of queries at a time
+                uint4 y[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = r0 + 8 * i, gr = w.p.qt * kP32Rows + r, tok = a.group.quot(gr);
-                    x[i] = load16(static_cast<const float *>(a.q) + 4 * lane +
+                    const int r = q0 + 8 * i, gr = w.p.qt * kP32Rows + r, tok = a.group.quot(gr);
+                    y[i] = load16(static_cast<const float *>(a.q) + 4 * lane +
                                       (r < rows ? (int64_t)(w.s.row0 + tok) * a.q_st +
                                                       (int64_t)(w.p.h * a.group.d + gr - tok * a.group.d) * a.q_sh
                                                 : 0),
                                   r < rows);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) put(qs, kP32QPart, r0 + 8 * i, x[i], flip);
+                for (int i = 0; i < 4; ++i) put(qs, kP32QPart, q0 + 8 * i, y[i], flip);
             }
             hand_over(q_full);
             for (int jt = w.j0; jt < w.j1; ++jt, ++g) {
-                const bool more = jt + 1 < w.j1;
-                if (g > 0) wait(k_empty, g - 1);
+                if (g > 0) wait(empty, g - 1);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) put(ks, kP32KPart, bw + 8 * i, kr[i], 1.f);
-                hand_over(k_full);
-                if (more) {
-                    locate(jt + 1);
-                    load(kp, a.k_sp, a.k_sh, a.k_sn, kr);
-                }
-                if (g > 0) wait(pv_done, g - 1);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) put(vs, kP32KPart, bw + 8 * i, vr[i], 1.f);
-                hand_over(v_full);
-                if (more) load(vp, a.v_sp, a.v_sh, a.v_sn, vr);
+                for (int i = 0; i < 16; ++i) put(tile, kP32KPart, r0 + 4 * i, x[i], 1.f);
+                hand_over(full);
+                if (jt + 1 < w.j1) load(jt + 1);
             }
         }
         if (cut) finish_last(cut_s, cut_p);
