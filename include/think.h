@@ -393,7 +393,7 @@ think_status_t think_gather_tokens(const void *x, const int64_t x_strides[3], in
  * holds the keys, another the values: the row of page p, head h and row i lies
  * at cache + p*strides[0] + h*strides[1] + i*strides[2], its 128 channels
  * contiguous.  Pages may be [page][head][row][128] or [page][row][head][128] or
- * any other strides that are multiples of 16 bytes.  Position n of request b
+ * any other strides above 0 that are multiples of 16 bytes.  Position n of request b
  * lies in page block_table[b*table_ld + n / page_size], row n % page_size; its
  * slot is page * page_size + row.  max_blocks entries of a table row may be
  * used (table_ld >= max_blocks); max_blocks * page_size <= 2^30.  The new tokens
@@ -466,7 +466,8 @@ think_status_t think_norm_rope_append(const void *q, const int64_t q_strides[2],
  *   q, out   [T][Hq][d] of dtype, strides of the token and the head.  Rows
  *            outside every request's range are not written.
  *   max_new  the largest number of new tokens of a request, or 0 if not
- *            known: it only helps to choose the kernel.
+ *            known: a hint, on which no result depends (the kernels built now
+ *            choose by the lengths on the device alone).
  *   Keys and values of positions < kv_lens[b] must be finite; what the pages
  * hold behind them, and pages that no row sees (before the window, behind the
  * last token), may be anything, their table entries too.  A needed page outside
@@ -477,7 +478,9 @@ think_status_t think_norm_rope_append(const void *q, const int64_t q_strides[2],
  * use: it begins with the status word and counters that every call leaves at
  * zero, at the same place whatever the shape, so that one workspace serves calls
  * of any shape it is large enough for, captured ones too; use it for this call
- * alone.  Results do not depend on timing.  Any Hq that is a multiple of Hkv (G <= 4096). */
+ * alone, by one call at a time.  A time-out (THINK_DEVICE_TIMEOUT_* bits) can
+ * leave counters: zero the workspace again after one.  Results do not depend on
+ * timing.  Any Hq that is a multiple of Hkv (G <= 4096). */
 size_t think_paged_attn_workspace_size(int64_t T, int Hq, int Hkv, int d, think_dtype_t dtype);
 think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const void *k_cache,
                                 const int64_t k_cache_strides[3], const void *v_cache, const int64_t v_cache_strides[3],

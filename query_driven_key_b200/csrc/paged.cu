@@ -230,7 +230,7 @@ think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const
     if (B < 0 || T < 0 || Hq < 0 || Hkv < 0 || window < 0 || max_new < 0 || !dtype_ok(dtype)) return THINK_ERR_INVALID_ARG;
     if (d != kD) return THINK_ERR_UNSUPPORTED;
     if (B == 0 || T == 0 || Hkv == 0) return THINK_OK;
-    if (Hq < Hkv || Hq % Hkv != 0 || !std::isfinite(scale)) return THINK_ERR_INVALID_ARG;
+    if (Hq < Hkv || Hq % Hkv != 0 || !std::isfinite(scale * 1.44269504088896341f)) return THINK_ERR_INVALID_ARG;
     const int G = Hq / Hkv;
     if (Hkv > 65535 || G > 4096 || T > INT32_MAX || T * G > INT32_MAX - 4096) return THINK_ERR_UNSUPPORTED;
     const think_status_t rc = check_table(block_table, table_ld, max_blocks, page_size, num_pages);
@@ -262,7 +262,8 @@ think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const
     a.v_sp = num_pages > 1 ? v_cache_strides[0] : kD, a.v_sh = Hkv > 1 ? v_cache_strides[1] : kD, a.v_sn = v_cache_strides[2];
     a.table_ld = table_ld;
     a.B = B, a.T = (int)T, a.Hkv = Hkv, a.group = Divisor(G), a.page = Divisor(page_size);
-    a.num_pages = num_pages, a.limit = max_blocks * page_size, a.window = window;
+    a.num_pages = num_pages, a.limit = max_blocks * page_size;
+    a.window = window < kMaxPosition ? window : 0;  // (every key is within such a window)
     a.rows_cap = p.rows_cap, a.parts = kTargetSMs, a.sides = p.sides;
     a.scale_log2 = scale * 1.44269504088896341f;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

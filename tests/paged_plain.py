@@ -109,7 +109,8 @@ def attend_bound(out, size, logit, dtype, keys: int):
     """How far the library's attention may be from `attend`, element by element.
 
     fp32 steps (unit u = 2^-24): a logit is a sum of 128 products in fp32, off by at most 128 u times the sum of their
-    magnitudes (`logit`); a weight is the exponential of it (the argument's own rounding after the maximum is taken off:
+    magnitudes (`logit`); the same holds where the products are formed from bf16 parts (fp32 tensors: 48 sums of 16
+    products on the tensor core, each off by at most 2 u, and the parts' products that are left out, below 2 u: 98 u); a weight is the exponential of it (the argument's own rounding after the maximum is taken off:
     another 2 u |z| <= 2 u logit each for z and the maximum; the exponential itself to 2^-20), so its relative error is
     below r = 132 u logit + 2^-20.  Numerator and denominator each carry r, and sums over `keys` terms and as many
     rescalings add 2 keys u.  So |err| <= (2 r + 4 keys u) * size.

@@ -232,6 +232,15 @@ def test_attn_rows_that_see_nothing(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+def test_attn_widest_window(dtype):
+    """A window wider than any position hides nothing, rows before position 0 included."""
+    x = P.Batch([6, 300], [0, 500], 4, 2, 16, dtype, 5, lens=[2, 800])
+    want = run_attn(x, 4, 2)
+    for x.window in (2 ** 30 - 1, 2 ** 30, 2 ** 31 - 1):
+        assert torch.equal(run_attn(x, 4, 2), want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_attn_large_logits(dtype):
     """Sharp softmax: maxima that grow along the keys, and weights that underflow."""
     x = P.Batch([40, 1], [700, 900], 8, 2, 32, dtype, 4, key_scale=12.0)
