@@ -6,7 +6,11 @@
 // bits each).  A product of two such sums, without the terms below 2^-24 of
 // it, is
 //     x0 y2 + x2 y0 + x1 y1 + x0 y1 + x1 y0 + x0 y0,
-// six bf16 products with fp32 sums, added from the smallest on.  Both products
+// six bf16 products with fp32 sums, added from the smallest on.  The tensor
+// core's sums lose up to a unit of the last place a step, towards zero: the small
+// terms of O have an accumulator of their own, so that O itself takes 4 steps a
+// tile and not 24 (error of 400 rows over 2400 keys against 64 bits 1.3e-6 with
+// one accumulator).  Both products
 // of the attention are formed that way, at a sixth of the bf16
 // rate, which is several times the rate of the FMA pipes:
 //     S = Q K^T      128 query rows x 64 keys; the parts of Q, K in shared memory
@@ -101,7 +105,7 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
     tc05::fence_before_sync();
     __syncthreads();
     tc05::fence_after_sync();
-    const uint32_t tmem = bars.tmem;  // S 0 .. 127 (two buffers), O 128 .. 255, P 256 .. 351 (three parts)
+    const uint32_t tmem = bars.tmem;  // S 0 .. 127 (two buffers), O 128 .. 255, P 256 .. 351 (three parts), small terms of O 352 .. 479
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t phase) {  // false from the first wait that runs out on
         if (ok) ok = pt_wait(bar, phase & 1, abort_flag, a.status, THINK_DEVICE_TIMEOUT_FULL);
@@ -159,9 +163,9 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
                     for (int i = 0; i < 6; ++i)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            tc05::mma_bf16_ts(tmem + 128u, tmem + 256u + 32u * term_left(i) + 8u * k,
+                            tc05::mma_bf16_ts(tmem + (i < 5 ? 352u : 128u), tmem + 256u + 32u * term_left(i) + 8u * k,
                                               v_desc + (((uint32_t)term_right(i) * kP32KPart + 2048u * k) >> 4), idesc_o,
-                                              more || i > 0 || k > 0);
+                                              more || (i > 0 && i < 5) || k > 0);
                     tc05::commit(pv_done);
                 }
             }
@@ -252,7 +256,8 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
         if (cut) finish_last(cut_s, cut_p);
     } else {
         // ----------------------------------------------------------- softmax
-        const uint32_t lane_addr = tmem + ((uint32_t)(32 * warp) << 16), o_addr = lane_addr + 128u, p_addr = lane_addr + 256u;
+        const uint32_t lane_addr = tmem + ((uint32_t)(32 * warp) << 16), o_addr = lane_addr + 128u, p_addr = lane_addr + 256u,
+                       low_addr = lane_addr + 352u;
         const float sl = fmaxf(fabsf(a.scale_log2), 1.0e-30f);  // a scale of 0 still sends -inf to -inf
         uint32_t g = 0;  // tiles of the part
         for (W w(a, plan_sm, parts, part); w.live(); w.next()) {
@@ -305,13 +310,14 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
                     tc05::fence_after_sync();
                     if (jt > w.j0 && __any_sync(0xffffffffu, grow)) {
 #pragma unroll 1
-                        for (int i = 0; i < 8; ++i) {
+                        for (int i = 0; i < 16; ++i) {
+                            const uint32_t at16 = (i < 8 ? o_addr : low_addr) + 16u * (i & 7);
                             uint32_t o[16];
-                            tc05::tmem_ld16_issue(o_addr + 16u * i, o);
+                            tc05::tmem_ld16_issue(at16, o);
                             tc05::tmem_ld_wait(o);
 #pragma unroll
                             for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-                            tc05::tmem_st16(o_addr + 16u * i, o);
+                            tc05::tmem_st16(at16, o);
                         }
                     }
 #pragma unroll
@@ -343,10 +349,14 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
                 float *pt = part_at(a, part, w.head ? 1 : 0, 0) + tid;  // element x of the row at pt[x * rows_cap]
 #pragma unroll 1
                 for (int i = 0; i < 4; ++i) {
-                    uint32_t o[32];
+                    uint32_t o[32], low[32];
                     tc05::tmem_ld32_issue(o_addr + 32u * i, o);
+                    tc05::tmem_ld32_issue(low_addr + 32u * i, low);
                     tc05::tmem_ld32_wait(o);
+                    tc05::tmem_ld32_keep(low);
                     if (!real) continue;
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(low[c]));
                     if (w.whole) {
 #pragma unroll
                         for (int c = 0; c < 32; c += 4)
