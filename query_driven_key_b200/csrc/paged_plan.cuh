@@ -363,7 +363,11 @@ __device__ __forceinline__ void store_out(__nv_bfloat16 *p, const float (&x)[N])
 // has few rows and up to hundreds of partials each), then four rows of four
 // channels a thread (of one with few rows, so that more threads share them):
 // rows are the partials' fast dimension, a thread's loads are 16 bytes, and none
-// waits for another one.  Bound by the bytes that one block has in flight.  The
+// waits for another one.  Bound by the bytes that one block has in flight: the
+// join of 18 partials of 4 rows ends about 10 us after the last keys of a decode
+// at 131072 tokens.  As a launch of its own after the attention: 52 instead of
+// 54 us for 3 fp32 chunks, but 211 instead of 194 for 32 single tokens and 13.8
+// instead of 9.0 for one short request.  The
 // order of the sums is fixed, so that the result does not depend on timing.
 // Called by NT threads with sync() as their barrier.
 struct MergeSmem {

@@ -78,8 +78,11 @@ __device__ __forceinline__ int64_t block_scan_i64(int64_t x, int64_t *ws, int64_
 // row is a new token, so that token's thread writes the table entry, and no
 // thread reads an entry that another one writes.  kv_lens and free_count may be
 // the outputs themselves: the blocks are then one cluster, and every block has
-// read a chunk's lengths before block 0 writes them.  Bound by latency: a few dependent loads, two
-// scans of ten shuffles and the stores.
+// read a chunk's lengths before block 0 writes them.
+// Bound by latency: a few dependent loads, two scans of ten shuffles and the
+// stores.  Measured: 256 requests of one token 4.3 us, 33 prompts (40 thousand
+// tokens, 0.5 MB) 6.2 us; an empty launch takes 2 to 3.  One token a thread
+// and one block took 5.3 and 13.9.
 template <int NT>
 __global__ void __launch_bounds__(NT, 1) extend_pages_kernel(const ExtendArgs a)
 {
@@ -191,6 +194,8 @@ __global__ void __launch_bounds__(NT, 1) extend_pages_kernel(const ExtendArgs a)
 // for n < kv_lens[b], zero behind it (zero keys add nothing to a channel's
 // energy) and for pages outside the pool.  A copy, bound by HBM: one 16-byte
 // vector a lane, kGatherRows rows a thread, all loaded before the first store.
+// Measured: 131072 tokens of 8 bf16 heads (537 MB) 83.3 us = 6.45 TB/s, the rate
+// of a plain copy; 5 requests of up to 1300 tokens (16 MB) 3.8 us.
 constexpr int kGatherThreads = 256;
 constexpr int kGatherRows = 4;
 

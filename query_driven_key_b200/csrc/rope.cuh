@@ -20,6 +20,10 @@
 // all heads of a token share them).  The angle is formed and reduced in fp64:
 // at position 131072 an fp32 product is off by up to 2^-24 * 131072 = 0.008 rad.
 // All arithmetic after it is fp32, with one rounding at the store.
+// Measured: 8192 tokens of 32 + 8 + 8 bf16 heads (201 MB) 42.9 us = 4.7 TB/s;
+// 1777 tokens of 12 + 4 + 4 fp32 heads (36 MB) 8.8 us; one token 3.6 us.  Rows
+// held in registers instead of the ring (90 a thread, two blocks an SM) 90, the
+// ring without fixed heads a thread 65, with three blocks of fewer threads 44.
 #pragma once
 
 #include "ptx.cuh"

@@ -32,7 +32,7 @@ def test_sizes():
     assert qdk.think_extend_pages_workspace_size() == 256
     size = qdk.think_paged_attn_workspace_size
     assert size(1, 32, 8) < size(16, 32, 8) < size(32, 32, 8) == size(4096, 32, 8) == size(4096, 8, 8)
-    assert 0 < size(64, 8, 8, dtype=torch.float32) == size(5000, 32, 8, dtype=torch.float32) < size(4096, 8, 8)
+    assert 0 < size(64, 8, 8, dtype=torch.float32) < size(128, 8, 8, dtype=torch.float32) == size(5000, 32, 8, dtype=torch.float32) < size(4096, 8, 8)
     assert size(10, 30, 8) == 0 and size(10, 32, 8, d=64) == 0 and size(10, 4, 8) == 0
 
 
