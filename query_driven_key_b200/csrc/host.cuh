@@ -113,44 +113,51 @@ EncodeTiledFn encode_fn()
 // the encoding (a decode step re-encodes the same two maps otherwise).
 struct MapKey {
     const void *base;
-    uint64_t dims[4], strides[3];
-    uint32_t box[3];
+    cuuint64_t dims[5], strides[4];
+    uint32_t box[5];
     int dtype, swizzle;
 };
 
 bool map_cache_find(const MapKey &k, CUtensorMap *m);
 void map_cache_put(const MapKey &k, const CUtensorMap &m);
 
-// 4-D map over (x, y, z, w) with element strides sy, sz, sw for y, z, w; box (bx, by, bz, 1).
-bool make_map_4d(CUtensorMap *m, think_dtype_t dt, const void *base, uint64_t dx, uint64_t dy,
-                 uint64_t dz, uint64_t dw, int64_t sy, int64_t sz, int64_t sw, uint32_t bx,
-                 uint32_t by, bool swizzle128 = false, uint32_t bz = 1)
+// Map of `rank` (4 or 5) dimensions, strides in elements for all but the first.
+bool make_map(CUtensorMap *m, think_dtype_t dt, const void *base, int rank, const uint64_t *dims, const int64_t *strides,
+              const uint32_t *box, bool swizzle128)
 {
     MapKey key;
     memset(&key, 0, sizeof(key));
     key.base = base;
-    key.dims[0] = dx, key.dims[1] = dy, key.dims[2] = dz, key.dims[3] = dw;
-    key.strides[0] = (uint64_t)sy, key.strides[1] = (uint64_t)sz, key.strides[2] = (uint64_t)sw;
-    key.box[0] = bx, key.box[1] = by, key.box[2] = bz;
+    for (int i = 0; i < rank; ++i) key.dims[i] = dims[i], key.box[i] = box[i];
+    for (int i = 0; i + 1 < rank; ++i) key.strides[i] = (uint64_t)strides[i];
     key.dtype = (int)dt;
     key.swizzle = swizzle128 ? 1 : 0;
     if (map_cache_find(key, m)) return true;
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const size_t es = esize(dt);
-    cuuint64_t dims[4] = {dx, dy, dz, dw};
-    cuuint64_t strides[3] = {(cuuint64_t)sy * es, (cuuint64_t)sz * es, (cuuint64_t)sw * es};
-    cuuint32_t box[4] = {bx, by, bz, 1};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
+    cuuint64_t bytes[4];
+    for (int i = 0; i + 1 < rank; ++i) bytes[i] = (cuuint64_t)strides[i] * esize(dt);
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     const CUresult r = fn(m, dt == THINK_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
-                          4, const_cast<void *>(base), dims, strides, box, estr,
+                          (cuuint32_t)rank, const_cast<void *>(base), key.dims, bytes, box, estr,
                           CU_TENSOR_MAP_INTERLEAVE_NONE,
                           swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return false;
     map_cache_put(key, *m);
     return true;
+}
+
+// 4-D map over (x, y, z, w) with element strides sy, sz, sw for y, z, w; box (bx, by, bz, 1).
+bool make_map_4d(CUtensorMap *m, think_dtype_t dt, const void *base, uint64_t dx, uint64_t dy,
+                 uint64_t dz, uint64_t dw, int64_t sy, int64_t sz, int64_t sw, uint32_t bx,
+                 uint32_t by, bool swizzle128 = false, uint32_t bz = 1)
+{
+    const uint64_t dims[4] = {dx, dy, dz, dw};
+    const int64_t strides[3] = {sy, sz, sw};
+    const uint32_t box[4] = {bx, by, bz, 1};
+    return make_map(m, dt, base, 4, dims, strides, box, swizzle128);
 }
 
 constexpr int kMapCacheSize = 16;

@@ -7,6 +7,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <numeric>
 
 #include "host.cuh"
 #include "paged_plan.cuh"
@@ -62,10 +63,28 @@ PagedPlan plan_paged(think_dtype_t dtype, int64_t T, int G)
     return p;
 }
 
+// Map of a cache for loads of `chunk` rows: (64 channels, 8 rows, 2 halves, page_size
+// / 8 groups of rows, (page, head)).  The last one steps by what divides both the
+// pages' and the heads' stride.
+think_status_t make_cache_map(CUtensorMap *m, PtOuter *outer, const PagedArgs &a, const void *base, int64_t sp, int64_t sh,
+                              int64_t sn, int chunk)
+{
+    const int64_t g = a.num_pages == 1 ? (a.Hkv == 1 ? kD : sh) : a.Hkv == 1 ? sp : std::gcd(sp, sh);
+    const int64_t page = a.num_pages == 1 ? 0 : sp / g, head = a.Hkv == 1 ? 0 : sh / g;
+    if (page > INT32_MAX || head > INT32_MAX || (a.num_pages - 1) * page + (a.Hkv - 1) * head >= INT32_MAX)
+        return THINK_ERR_UNSUPPORTED;
+    const int64_t n = (a.num_pages - 1) * page + (a.Hkv - 1) * head + 1;
+    *outer = {(int)page, (int)head, (int)n};
+    const uint64_t dims[5] = {64, 8, 2, (uint64_t)a.page.d / 8, (uint64_t)n};
+    const int64_t strides[4] = {sn, 64, 8 * sn, g};
+    const uint32_t box[5] = {64, 8, 2, (uint32_t)chunk / 8, 1};
+    return make_map(m, THINK_BF16, base, 5, dims, strides, box, true) ? THINK_OK : THINK_ERR_CUDA;
+}
+
 think_status_t launch_paged_tc(const PagedArgs &a, cudaStream_t st)
 {
-    // rows of one TMA load: the largest power of two that divides the page, at most a tile
-    const int chunk = std::min(kPtBN, a.page.d & -a.page.d);
+    // rows of one TMA load: the largest power of two that divides the page, at most half a tile
+    const int chunk = std::min(kPtBN / 2, a.page.d & -a.page.d);
     // a tile's 128 query rows, tokens x heads of a group, as one TMA box; not if
     // the group does not divide them, a negative scale turns them on the way, or
     // the strides are none of TMA's
@@ -73,15 +92,16 @@ think_status_t launch_paged_tc(const PagedArgs &a, cudaStream_t st)
     const auto fits = [](int64_t stride, int n) { return n == 1 || (stride > 0 && stride < ((int64_t)1 << 39)); };
     const bool tma_q = 128 % G == 0 && a.scale_log2 >= 0.f && fits(a.q_sh, Hq) && fits(a.q_st, a.T);
     CUtensorMap mk, mv, mq;
-    if (!make_map_4d(&mk, THINK_BF16, a.k, kD, a.page.d, a.Hkv, a.num_pages, a.k_sn, a.k_sh, a.k_sp, 64, chunk, true) ||
-        !make_map_4d(&mv, THINK_BF16, a.v, kD, a.page.d, a.Hkv, a.num_pages, a.v_sn, a.v_sh, a.v_sp, 64, chunk, true))
-        return THINK_ERR_CUDA;
+    PtOuter ok, ov;
+    think_status_t rc = make_cache_map(&mk, &ok, a, a.k, a.k_sp, a.k_sh, a.k_sn, chunk);
+    if (rc == THINK_OK) rc = make_cache_map(&mv, &ov, a, a.v, a.v_sp, a.v_sh, a.v_sn, chunk);
+    if (rc != THINK_OK) return rc;
     // (the stride of a dimension of one element is free)
     if (!tma_q) mq = mk;
     else if (!make_map_4d(&mq, THINK_BF16, a.q, kD, Hq, a.T, 1, Hq > 1 ? a.q_sh : kD, a.T > 1 ? a.q_st : kD, kD, 64, G, true, 128 / G))
         return THINK_ERR_CUDA;
     if (!ensure_smem(reinterpret_cast<const void *>(&paged_tc_kernel), paged_tc_smem())) return THINK_ERR_CUDA;
-    return launch_pdl(paged_tc_kernel, dim3(kTargetSMs), dim3(kPtThreads), paged_tc_smem(), st, mk, mv, mq, a, chunk, tma_q);
+    return launch_pdl(paged_tc_kernel, dim3(kTargetSMs), dim3(kPtThreads), paged_tc_smem(), st, mk, mv, mq, a, ok, ov, chunk, tma_q);
 }
 
 think_status_t launch_paged_tc32(const PagedArgs &a, cudaStream_t st)
@@ -243,10 +263,10 @@ think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const
         !aligned4(q_start) || !aligned4(kv_lens) || !strides16(q_strides, 2, es) || !strides16(out_strides, 2, es) ||
         !strides16(k_cache_strides, 3, es) || !strides16(v_cache_strides, 3, es))
         return THINK_ERR_ALIGNMENT;
-    for (const int64_t *c : {k_cache_strides, v_cache_strides})  // TMA: strides above 0 and below 2^40 bytes
+    for (const int64_t *c : {k_cache_strides, v_cache_strides})  // TMA: strides (eight rows' too) above 0 and below 2^40 bytes
         for (int i = 0; i < 3; ++i) {
             if (c[i] == 0 && (i == 0 ? num_pages : i == 1 ? Hkv : page_size) > 1) return THINK_ERR_INVALID_ARG;
-            if (c[i] >= ((int64_t)1 << 40) / (int64_t)es) return THINK_ERR_UNSUPPORTED;
+            if (c[i] >= ((int64_t)1 << (i < 2 ? 40 : 37)) / (int64_t)es) return THINK_ERR_UNSUPPORTED;
         }
     const PagedPlan p = plan_paged(dtype, T, G);
     if (workspace_bytes < p.ws_bytes) return THINK_ERR_WORKSPACE;

@@ -19,10 +19,11 @@
 // joined at its end.
 //
 // Keys and values come by TMA, page by page: a load moves `chunk` rows (the
-// largest power of two that divides page_size, at most 128) of one 64-channel
-// half, so that no load crosses a page, into a ring of 32 KB stages with the
-// 128-byte swizzle; chunks that no row of the item sees (and pages outside the
-// pool) are loaded from behind the pool's end, which TMA fills with zeros.
+// largest power of two that divides page_size, at most 64), so that no load
+// crosses a page, into a ring of 32 KB stages with the 128-byte swizzle.  A tile
+// lies there as [8 rows][64-channel half][row][64 channels], so that one load
+// brings both halves of a chunk: the cost of many small loads is a load's, not a
+// byte's (a load a half took 207 us for the batch of single tokens below).  Chunks that no row of the item sees (and pages outside the pool) are loaded from behind the pool's end, which TMA fills with zeros.
 // Value rows behind the request's last token are set to zero in shared memory
 // before their product, whatever the page holds there.
 //
@@ -36,7 +37,7 @@
 // the softmax between the two products, which share a TMEM region and hence
 // alternate for a warpgroup; the other one's fill the gap.  Measured: 131072
 // keys of 8 heads, one token (537 MB) 104 us = 5.2 TB/s; 32 requests of 500 to
-// 16000 keys in pages of 16 (978 MB) 205 us = 4.8 TB/s; a prompt of 16384 tokens
+// 16000 keys in pages of 16 (978 MB) 191 us = 5.1 TB/s; a prompt of 16384 tokens
 // and 32 heads (2.2 TFLOP) 2.01 ms = 1.09 PFLOP/s, at the power cap; 13 requests
 // with a window (0.21 TFLOP) 250 us.  One product warp for both warpgroups
 // took 2.70 ms for the prompt, 16 softmax warps (two threads a row) 2.19,
@@ -191,9 +192,15 @@ struct PtOrder {
     }
 };
 
+// Where a (page, head) lies along a cache map's last dimension; `none` is behind its end.
+struct PtOuter {
+    int page, head, none;
+};
+
 __global__ void __launch_bounds__(kPtThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                    const __grid_constant__ CUtensorMap tm_q, const PagedArgs a, const int chunk, const bool tma_q)
+                    const __grid_constant__ CUtensorMap tm_q, const PagedArgs a, const PtOuter outer_k,
+                    const PtOuter outer_v, const int chunk, const bool tma_q)
 {
     using W = Walk<kPtRows, kPtBN>;
     extern __shared__ unsigned char smem_dyn[];
@@ -247,11 +254,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kPtProducer || warp == kPtMma + 2) {
         // --------------------------------------------------------- producers
-        // A warp a 64-channel half, a lane a chunk: a warp's lanes issue their
-        // loads one after another, and with 16-row pages a tile has 8 of each half.
-        const int half = warp != kPtProducer;
-        const int per_tile = kPtBN / chunk;
-        const uint32_t bytes = (uint32_t)chunk * 128u;
+        // A warp half of a tile's rows, a lane a chunk: a warp's lanes issue their
+        // loads one after another, and with 16-row pages a tile has 8.
+        const int per_warp = kPtBN / 2 / chunk;
+        const int chunk0 = lane + (warp != kPtProducer ? per_warp : 0);
+        const uint32_t bytes = (uint32_t)chunk * 256u;
         uint32_t ld = 0;                     // loads issued: stage ld % kPtStages
         uint32_t phases = 0, used = 0;       // of each full barrier its next phase; of each stage the last one's set
         bool ok = true;
@@ -263,8 +270,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             // row in the page
             auto locate = [&](int i, int &entry, int &row, bool &needed, bool &value, int &tile) {
                 tile = order.tile(i, value);
-                const int key = (w.j0 + tile) * kPtBN + lane * chunk;
-                needed = lane < per_tile && key < w.t.hi && key + chunk > w.t.lo;
+                const int key = (w.j0 + tile) * kPtBN + chunk0 * chunk;
+                needed = lane < per_warp && key < w.t.hi && key + chunk > w.t.lo;
                 const int j = a.page.quot(key);
                 row = key - j * a.page.d;
                 entry = needed ? a.table[(int64_t)w.p.b * a.table_ld + j] : -1;
@@ -285,12 +292,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 used = (used & ~(3u << (2 * s))) | set << (2 * s);
                 if (lane == 0) mbar_arrive_expect_tx(full, kPtTile / 2);
                 __syncwarp();
-                if (lane < per_tile) {
+                if (lane < per_warp) {
                     const bool inside = cur_needed && (unsigned)cur_entry < (unsigned)a.num_pages;
                     if (cur_needed && !inside) atomicOr(a.status, THINK_DEVICE_BAD_PAGE);
-                    tma_load_4d(smem_addr(ring + s * kPtTile) + (uint32_t)half * 16384u + (uint32_t)lane * bytes,
-                                cur_value ? &tm_v : &tm_k, half * 64, inside ? cur_row : 0, w.p.h,
-                                inside ? cur_entry : a.num_pages, full);
+                    const PtOuter outer = cur_value ? outer_v : outer_k;
+                    tma_load_5d(smem_addr(ring + s * kPtTile) + (uint32_t)chunk0 * bytes, cur_value ? &tm_v : &tm_k, 0, 0, 0,
+                                inside ? cur_row / 8 : 0, inside ? cur_entry * outer.page + w.p.h * outer.head : outer.none,
+                                full);
                 }
             }
         }
@@ -322,8 +330,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (ok) ok = pt_wait(bar, phase & 1, abort_flag, a.status, code);
         };
         const uint64_t q_desc = tc05::smem_desc(smem_addr(qs), 16u, 1024u, tc05::kLayoutSwizzle128B);
-        const uint64_t k_desc = tc05::smem_desc(smem_addr(ring), 16u, 1024u, tc05::kLayoutSwizzle128B);
-        const uint64_t v_desc = tc05::smem_desc(smem_addr(ring), 16384u, 1024u, tc05::kLayoutSwizzle128B);
+        const uint64_t k_desc = tc05::smem_desc(smem_addr(ring), 16u, 2048u, tc05::kLayoutSwizzle128B);
+        const uint64_t v_desc = tc05::smem_desc(smem_addr(ring), 1024u, 2048u, tc05::kLayoutSwizzle128B);
         const uint32_t s_tmem = uniform(tmem + 128u * t), o_tmem = s_tmem + 256u;
         const uint32_t s_bar = uniform(sfull0 + 8 * t), o_bar = uniform(ofull0 + 8 * t);
         for (W w(a, plan_sm, parts, part); w.live() && ok; w.next()) {
@@ -352,8 +360,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 if (leader) {
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
-                        const uint32_t o = ((uint32_t)(ks >> 2) * 16384u + (uint32_t)(ks & 3) * 32u) >> 4;
-                        tc05::mma_bf16(s_tmem, qd + o, kd + o, idesc_s, ks > 0);
+                        const uint32_t o = (uint32_t)(ks & 3) * 32u;
+                        tc05::mma_bf16(s_tmem, qd + (((uint32_t)(ks >> 2) * 16384u + o) >> 4),
+                                       kd + (((uint32_t)(ks >> 2) * 1024u + o) >> 4), idesc_s, ks > 0);
                     }
                     tc05::commit(s_bar);
                 }
@@ -392,9 +401,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 const int from = max(0, w.s.kv - (w.j0 + j) * kPtBN);
                 if (from < kPtBN) {
                     unsigned char *v = ring + s * kPtTile;
-                    for (int c = lane; c < (kPtBN - from) * 8; c += 32) {
-                        *reinterpret_cast<uint4 *>(v + from * 128 + c * 16) = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4 *>(v + 16384 + from * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+                    for (int c = lane; c < (kPtBN - from) * 16; c += 32) {
+                        const int i = from + (c >> 4);
+                        *reinterpret_cast<uint4 *>(v + (i >> 3) * 2048 + (c & 8) * 128 + (i & 7) * 128 + (c & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
                     }
                     tc05::fence_proxy_async_smem();
                     __syncwarp();
@@ -409,7 +419,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     if (leader) {
 #pragma unroll
                         for (int ks = k0; ks < k1; ++ks)
-                            tc05::mma_bf16_ts(o_tmem, s_tmem + 8u * ks, vd + 128u * ks, idesc_o, ks > 0 || more);
+                            tc05::mma_bf16_ts(o_tmem, s_tmem + 8u * ks, vd + 256u * ks, idesc_o, ks > 0 || more);
                     }
                 };
                 wait(turn0 + 8 * t, nt++, THINK_DEVICE_TIMEOUT_FULL);

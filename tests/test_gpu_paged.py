@@ -277,6 +277,29 @@ def test_attn_strides_and_views(dtype, Hq, Hkv):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("pad_page,pad_head", [(8, 0), (24, 40), (0, 8)])
+def test_attn_pages_and_heads_at_any_distance(dtype, pad_page, pad_head):
+    """Strides of pages and heads that are not multiples of one another."""
+    x = P.Batch([3, 40], [600, 130], 6, 3, 32, dtype, 41)
+
+    def spread(c):  # [pages,Hkv,page,128] with gaps of NaN behind each head and page
+        n, h, rows, d = c.shape
+        sh = rows * d + pad_head
+        sp = h * sh + pad_page
+        flat = torch.full((n * sp,), float("nan"), dtype=dtype, device="cuda")
+        out = torch.as_strided(flat, c.shape, (sp, sh, d, 1))
+        out.copy_(c)
+        return out
+
+    w = attn_ws(x.T, 6, 3, dtype)
+    out = torch.full((x.T, 6, 128), 9.0, dtype=dtype, device="cuda")
+    qdk.think_paged_attn(x.q.cuda(), spread(x.cache(x.k)), spread(x.cache(x.v)), i32(x.table), i32(x.q_start), i32(x.lens), out, w,
+                         scale=SCALE)
+    assert qdk.think_read_device_status(w) == 0
+    assert torch.equal(out, run_attn(x, 6, 3))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_attn_bad_pages_count_as_zeros(dtype):
     x = P.Batch([5, 40], [200, 90], 4, 2, 32, dtype, 9, poison=False)
     x.table[0][2], x.table[1][1] = -1, x.k.shape[0]
