@@ -8,7 +8,7 @@
 // rows that see nothing are still written) and a fixed cost.  The items' units
 // form one sequence, requests first, then heads, then row tiles; block i of P
 // takes the i-th of P equal parts of it.  Whatever the mix of lengths, all blocks
-// get the same work to within a unit; an item that a part's border cuts is computed in
+// get the same work to within a unit or a short item, which is not cut; an item that a part's border cuts is computed in
 // pieces, each piece leaves its (max, sum, O) in the workspace, and the block
 // that finishes the last one joins them in order.  Lengths stay on the device: the plan is
 // recomputed from q_start and kv_lens by every launch, so that a captured
@@ -87,6 +87,10 @@ __device__ __forceinline__ TileRange tile_range(const PagedArgs &a, const Reques
 // 3: 2040, 4: 2024; the fp32 kernel's items cost less than one of its tiles.
 template <int R>
 constexpr int kItemCost = R == 256 ? 4 : 1;
+// The least units of a part: more parts only make for longer joins (one token over
+// 4000 keys with 4 units a part 18.0 us, with 1 19.8).
+template <int R>
+constexpr int kLeast = R == 256 ? 4 : 1;
 
 template <int R>
 __device__ __forceinline__ int row_tiles(const PagedArgs &a, const Request &s)
@@ -145,13 +149,26 @@ struct PlanSmem {
     Request request;  // of the place
 };
 
-// The sequence of `total` units in min(parts, total) parts, none of which is empty.
+// Items of up to so many key tiles are not cut: a join takes longer than their
+// tiles in one block.  (Tiles of items that the warpgroups share by keys take
+// half the time; an fp32 tile takes as long as a join.)  Measured, cut -> whole: 16
+// single tokens over 250 to 500 keys 29.0 -> 14.6 us, over 1000 to 2000 39.0 -> 34.2,
+// 64 over 500 to 1000 67.0 -> 58.8; a prompt of 400 tokens 26.7 -> 15.4, of 1000 37.2
+// -> 24.2.  Up to 24 tiles whole: one token over 4000 keys 18 -> 26.
+template <int R>
+__device__ __forceinline__ int uncut(int rows)
+{
+    return R == 256 ? (rows <= 128 ? 16 : 8) : 0;
+}
+
+// The sequence of `total` units in at most `parts` parts of at least `least`
+// units each (but for a rest).
 struct Parts {
     int64_t total, per;
     int n, rem;
-    __device__ __forceinline__ Parts(int64_t units, int parts) : total(units)
+    __device__ __forceinline__ Parts(int64_t units, int parts, int least) : total(units)
     {
-        n = (int)min((int64_t)parts, total);
+        n = (int)min((int64_t)parts, (total + least - 1) / least);
         per = n > 0 ? quot64(total, n) : 0;
         rem = (int)(total - per * n);
     }
@@ -190,7 +207,7 @@ __device__ __forceinline__ Parts plan(const PagedArgs &a, PlanSmem *sm, int part
             if (w == warp) before = total;
             total += sm->ws[w];
         }
-        const Parts parts(total, a.parts);
+        const Parts parts(total, a.parts, kLeast<R>);
         int64_t rem = parts.begin(part) - before;
         if (rem >= 0 && rem < uh * a.Hkv) {  // this warp's request holds the place
             Place p;
@@ -229,7 +246,7 @@ __device__ __forceinline__ Parts plan(const PagedArgs &a, PlanSmem *sm, int part
     int64_t total = 0;
     for (int w = 0; w < W; ++w) total += sm->ws[w];
     __syncthreads();
-    const Parts parts(total, a.parts);
+    const Parts parts(total, a.parts, kLeast<R>);
     const int64_t u = parts.begin(part);
     int64_t base = 0;
     for (int b0 = 0; b0 < a.B && base <= u; b0 += NT) {
@@ -290,8 +307,11 @@ struct Walk {
     __device__ __forceinline__ void set()
     {
         t = tile_range<R, BN>(a, s, p.qt);
-        j0 = t.j0 + max(0, p.off - kItemCost<R>);
-        j1 = (int)min((int64_t)t.j1, t.j0 + max((int64_t)0, p.off - kItemCost<R> + left));
+        // the part's borders, in key tiles; an item that is not cut is the part's that holds its end
+        const int n = t.j1 - t.j0, whole_to = n <= uncut<R>(s.n * a.group.d - p.qt * R) ? n - 1 : 0;
+        const int64_t to = p.off - kItemCost<R> + left;
+        j0 = t.j0 + (whole_to > 0 ? 0 : max(0, p.off - kItemCost<R>));
+        j1 = to >= n ? t.j1 : t.j0 + (to <= whole_to ? 0 : (int)to);
         head = j0 == t.j0;
         whole = head && j1 == t.j1;
         if (j0 == j1) left = 0;  // the part ends before the item's first tile
