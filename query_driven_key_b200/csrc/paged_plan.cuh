@@ -367,25 +367,47 @@ __device__ __forceinline__ void store_out(float *p, const float (&x)[N])
 template <int N>
 __device__ __forceinline__ void store_out(__nv_bfloat16 *p, const float (&x)[N])
 {
-    if constexpr (N == 4) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-        *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    if constexpr (N == 8) {
+        uint4 v;
+        __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(&v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        *reinterpret_cast<uint4 *>(p) = v;
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) p[i] = __float2bfloat16_rn(x[i]);
     }
 }
 
+// 16 bytes, zeros if not `real`.  (A volatile statement: a plain load would be
+// moved down to its use.)
+__device__ __forceinline__ float4 load_cg(const float *p, bool real)
+{
+    float4 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&f"(v.x), "=&f"(v.y), "=&f"(v.z), "=&f"(v.w)
+        : "l"(p), "r"((uint32_t)real)
+        : "memory");
+    return v;
+}
+
 // Join the pieces of an item, in the parts c0 .. c1:
 //     m = max m_i,  l = sum l_i 2^(m_i - m),  out = sum O_i 2^(m_i - m) / l.
 // A row that sees no key has l = 0 and gets zeros.  First m, l and the factors
 // of the partials, with as many lanes a row as the threads allow (a decode step
-// has few rows and up to hundreds of partials each), then four rows of four
-// channels a thread (of one with few rows, so that more threads share them):
-// rows are the partials' fast dimension, a thread's loads are 16 bytes, and none
-// waits for another one.  Bound by the bytes that one block has in flight: the
-// join of 18 partials of 4 rows ends about 10 us after the last keys of a decode
-// at 131072 tokens.  As a launch of its own after the attention: 52 instead of
+// has few rows and up to hundreds of partials each), then four rows of eight
+// channels a thread (four in the fp32 kernel, which has fewer registers; one with few
+// rows, so that more threads share them): rows are the partials' fast dimension, a
+// thread's loads are 16 bytes, and 8 to 16 of them are under way at a time.  Bound by
+// the bytes that one block has in flight, by the stores (8 channels a row: 16
+// bytes; 4 took 5 us more for chunks of 300 tokens), and by its code, which is cold:
+// the same loops unrolled further are slower.  131072 keys and one token, 36
+// partials of 4 rows: 7 us of 96; chunks of 300 tokens of 6 requests: 16 of 37.
+// As a launch of its own after the attention (an earlier form): 52 instead of
 // 54 us for 3 fp32 chunks, but 211 instead of 194 for 32 single tokens and 13.8
 // instead of 9.0 for one short request.  The
 // order of the sums is fixed, so that the result does not depend on timing.
@@ -464,30 +486,38 @@ __device__ __forceinline__ void merge_pieces(const PagedArgs &a, MergeSmem &sm, 
         }
     }
     sync();
-    auto channels = [&](auto width) {
-        constexpr int N = decltype(width)::value;
+    // N channels of four rows, from U partials at a time
+    auto channels = [&](auto width, auto partials) {
+        constexpr int N = decltype(width)::value, U = decltype(partials)::value;
+#pragma unroll 1
         for (int k = tid; k < quads * (kD / N); k += NT) {
             const int c = k / quads * N, q = k % quads;
             float4 o[N];
 #pragma unroll
             for (int j = 0; j < N; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll(N == 1 ? 8 : 4)
-            for (int i = 0; i < count; ++i) {
-                const float *y = at(i, 4 * q);
-                float4 g;
-                if (kept) {
-                    g = sm.g[i * quads + q];
-                } else {
-                    const float4 mi = __ldcg(reinterpret_cast<const float4 *>(y + kD * ld));
-                    const float4 m = *reinterpret_cast<const float4 *>(sm.m + 4 * q), inv = *reinterpret_cast<const float4 *>(sm.inv + 4 * q);
-                    g = make_float4(exp2f(mi.x - m.x) * inv.x, exp2f(mi.y - m.y) * inv.y, exp2f(mi.z - m.z) * inv.z,
-                                    exp2f(mi.w - m.w) * inv.w);
+#pragma unroll 1
+            for (int i0 = 0; i0 < count; i0 += U) {
+                float4 v[U][N], g[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = min(i0 + u, count - 1);  // (those behind the last are zeros)
+                    const float *y = at(i, 4 * q);
+#pragma unroll
+                    for (int j = 0; j < N; ++j) v[u][j] = load_cg(y + (c + j) * ld, i0 + u < count);
+                    if (kept) {
+                        g[u] = sm.g[i * quads + q];
+                    } else {
+                        const float4 mi = __ldcg(reinterpret_cast<const float4 *>(y + kD * ld));
+                        const float4 m = *reinterpret_cast<const float4 *>(sm.m + 4 * q), inv = *reinterpret_cast<const float4 *>(sm.inv + 4 * q);
+                        g[u] = make_float4(exp2f(mi.x - m.x) * inv.x, exp2f(mi.y - m.y) * inv.y, exp2f(mi.z - m.z) * inv.z,
+                                           exp2f(mi.w - m.w) * inv.w);
+                    }
                 }
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const float4 v = __ldcg(reinterpret_cast<const float4 *>(y + (c + j) * ld));
-                    o[j].x += v.x * g.x, o[j].y += v.y * g.y, o[j].z += v.z * g.z, o[j].w += v.w * g.w;
-                }
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int j = 0; j < N; ++j)
+                        o[j].x += v[u][j].x * g[u].x, o[j].y += v[u][j].y * g[u].y, o[j].z += v[u][j].z * g[u].z, o[j].w += v[u][j].w * g[u].w;
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -501,8 +531,9 @@ __device__ __forceinline__ void merge_pieces(const PagedArgs &a, MergeSmem &sm, 
             }
         }
     };
-    if (quads > 2) channels(std::integral_constant<int, 4>{});
-    else channels(std::integral_constant<int, 1>{});
+    using std::integral_constant;
+    if (quads > 2) channels(integral_constant<int, R == 256 ? 8 : 4>{}, integral_constant<int, 2>{});
+    else channels(integral_constant<int, 1>{}, integral_constant<int, 8>{});
 }
 
 // A piece's partial has been written by (some of) the calling NT threads: count it, and

@@ -36,10 +36,10 @@
 // Bound: single tokens by HBM (each key and value is read once), long chunks by
 // the softmax between the two products, which share a TMEM region and hence
 // alternate for a warpgroup; the other one's fill the gap.  Measured: 131072
-// keys of 8 heads, one token (537 MB) 104 us = 5.2 TB/s; 32 requests of 500 to
-// 16000 keys in pages of 16 (978 MB) 191 us = 5.1 TB/s; a prompt of 16384 tokens
-// and 32 heads (2.2 TFLOP) 2.01 ms = 1.09 PFLOP/s, at the power cap; 13 requests
-// with a window (0.21 TFLOP) 250 us.  One product warp for both warpgroups
+// keys of 8 heads, one token (537 MB) 100 us = 5.4 TB/s; 32 requests of 500 to
+// 16000 keys in pages of 16 (978 MB) 190 us = 5.1 TB/s; a prompt of 16384 tokens
+// and 32 heads (2.2 TFLOP) 1.99 ms = 1.10 PFLOP/s, at the power cap; 13 requests
+// with a window (0.21 TFLOP) 247 us.  One product warp for both warpgroups
 // took 2.70 ms for the prompt, 16 softmax warps (two threads a row) 2.19,
 // exponentials of a quarter of the keys by a polynomial 2.18; one producer
 // warp 233 us for the batch.

@@ -28,7 +28,7 @@
 // logits have two buffers in TMEM, so that the next tile's run beside this one's
 // softmax.  Bound by the products: 72 a tile, about 4100 cycles, and by a tile's
 // chain from logits to O, which only the next tile's logits overlap.  Measured:
-// 3 chunks of 90 to 400 tokens over up to 2900 keys, 8 heads (1.5 GFLOP) 54 us;
+// 3 chunks of 90 to 400 tokens over up to 2900 keys, 8 heads (1.5 GFLOP) 52 us;
 // on the FMA pipes with cp.async 102, and 61 without warps of their own for the
 // keys' and the values' parts.
 // Every wait is bounded, as in the bf16 kernel.
