@@ -393,7 +393,9 @@ think_status_t think_gather_tokens(const void *x, const int64_t x_strides[3], in
  * holds the keys, another the values: the row of page p, head h and row i lies
  * at cache + p*strides[0] + h*strides[1] + i*strides[2], its 128 channels
  * contiguous.  Pages may be [page][head][row][128] or [page][row][head][128] or
- * any other strides above 0 that are multiples of 16 bytes.  Position n of request b
+ * any other strides above 0 that are multiples of 16 bytes (think_paged_attn in bf16:
+ * the pool's extent in steps of the page and head strides' common divisor below
+ * 2^31).  Position n of request b
  * lies in page block_table[b*table_ld + n / page_size], row n % page_size; its
  * slot is page * page_size + row.  max_blocks entries of a table row may be
  * used (table_ld >= max_blocks); max_blocks * page_size <= 2^30.  The new tokens
@@ -422,7 +424,7 @@ think_status_t think_gather_tokens(const void *x, const int64_t x_strides[3], in
  * (those that fit) exceed *free_count.  The slot of a page number below 0
  * (in the table or the stack) is -1, with THINK_DEVICE_BAD_PAGE.
  *   kv_lens_out may be kv_lens and free_count_out may be free_count; no other
- * buffers may overlap.  workspace: think_extend_pages_workspace_size() bytes,
+ * buffers may overlap.  Without requests (B == 0) nothing is written.  workspace: think_extend_pages_workspace_size() bytes,
  * zeroed once (think_workspace_init); it holds the status word. */
 size_t think_extend_pages_workspace_size(void);
 think_status_t think_extend_pages(const int32_t *new_lens, const int32_t *kv_lens, int B, int page_size,
@@ -464,7 +466,8 @@ think_status_t think_norm_rope_append(const void *q, const int64_t q_strides[2],
  * gets zeros.  Arithmetic: fp32 sums and softmax; bf16 rounds the softmax
  * weights to bf16 before the product with V, as it rounds the output.
  *   q, out   [T][Hq][d] of dtype, strides of the token and the head.  Rows
- *            outside every request's range are not written.
+ *            outside every request's range are not written.  out may not overlap
+ *            q or the caches.
  *   max_new  the largest number of new tokens of a request, or 0 if not
  *            known: a hint, on which no result depends (the kernels built now
  *            choose by the lengths on the device alone).

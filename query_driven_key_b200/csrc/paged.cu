@@ -63,22 +63,28 @@ PagedPlan plan_paged(think_dtype_t dtype, int64_t T, int G)
     return p;
 }
 
+// How far a page and a head are along a cache map's last dimension, which steps by
+// what divides both strides.
+struct CacheSteps {
+    int64_t step, page, head, n;
+    CacheSteps(const PagedArgs &a, int64_t sp, int64_t sh)
+    {
+        step = a.num_pages == 1 ? (a.Hkv == 1 ? kD : sh) : a.Hkv == 1 ? sp : std::gcd(sp, sh);
+        page = a.num_pages == 1 ? 0 : sp / step, head = a.Hkv == 1 ? 0 : sh / step;
+        n = page > INT32_MAX || head > INT32_MAX ? INT64_MAX : (a.num_pages - 1) * page + (a.Hkv - 1) * head + 1;
+    }
+    bool ok() const { return n <= INT32_MAX; }
+    PtOuter outer() const { return {(int)page, (int)head, (int)n}; }
+};
+
 // Map of a cache for loads of `chunk` rows: (64 channels, 8 rows, 2 halves, page_size
-// / 8 groups of rows, (page, head)).  The last one steps by what divides both the
-// pages' and the heads' stride.
-think_status_t make_cache_map(CUtensorMap *m, PtOuter *outer, const PagedArgs &a, const void *base, int64_t sp, int64_t sh,
-                              int64_t sn, int chunk)
+// / 8 groups of rows, (page, head)).
+bool make_cache_map(CUtensorMap *m, const CacheSteps &x, const void *base, int64_t sn, int page_size, int chunk)
 {
-    const int64_t g = a.num_pages == 1 ? (a.Hkv == 1 ? kD : sh) : a.Hkv == 1 ? sp : std::gcd(sp, sh);
-    const int64_t page = a.num_pages == 1 ? 0 : sp / g, head = a.Hkv == 1 ? 0 : sh / g;
-    if (page > INT32_MAX || head > INT32_MAX || (a.num_pages - 1) * page + (a.Hkv - 1) * head >= INT32_MAX)
-        return THINK_ERR_UNSUPPORTED;
-    const int64_t n = (a.num_pages - 1) * page + (a.Hkv - 1) * head + 1;
-    *outer = {(int)page, (int)head, (int)n};
-    const uint64_t dims[5] = {64, 8, 2, (uint64_t)a.page.d / 8, (uint64_t)n};
-    const int64_t strides[4] = {sn, 64, 8 * sn, g};
+    const uint64_t dims[5] = {64, 8, 2, (uint64_t)page_size / 8, (uint64_t)x.n};
+    const int64_t strides[4] = {sn, 64, 8 * sn, x.step};
     const uint32_t box[5] = {64, 8, 2, (uint32_t)chunk / 8, 1};
-    return make_map(m, THINK_BF16, base, 5, dims, strides, box, true) ? THINK_OK : THINK_ERR_CUDA;
+    return make_map(m, THINK_BF16, base, 5, dims, strides, box, true);
 }
 
 think_status_t launch_paged_tc(const PagedArgs &a, cudaStream_t st)
@@ -92,16 +98,16 @@ think_status_t launch_paged_tc(const PagedArgs &a, cudaStream_t st)
     const auto fits = [](int64_t stride, int n) { return n == 1 || (stride > 0 && stride < ((int64_t)1 << 39)); };
     const bool tma_q = 128 % G == 0 && a.scale_log2 >= 0.f && fits(a.q_sh, Hq) && fits(a.q_st, a.T);
     CUtensorMap mk, mv, mq;
-    PtOuter ok, ov;
-    think_status_t rc = make_cache_map(&mk, &ok, a, a.k, a.k_sp, a.k_sh, a.k_sn, chunk);
-    if (rc == THINK_OK) rc = make_cache_map(&mv, &ov, a, a.v, a.v_sp, a.v_sh, a.v_sn, chunk);
-    if (rc != THINK_OK) return rc;
+    const CacheSteps ks(a, a.k_sp, a.k_sh), vs(a, a.v_sp, a.v_sh);
+    if (!ks.ok() || !vs.ok()) return THINK_ERR_UNSUPPORTED;
+    if (!make_cache_map(&mk, ks, a.k, a.k_sn, a.page.d, chunk) || !make_cache_map(&mv, vs, a.v, a.v_sn, a.page.d, chunk))
+        return THINK_ERR_CUDA;
     // (the stride of a dimension of one element is free)
     if (!tma_q) mq = mk;
     else if (!make_map_4d(&mq, THINK_BF16, a.q, kD, Hq, a.T, 1, Hq > 1 ? a.q_sh : kD, a.T > 1 ? a.q_st : kD, kD, 64, G, true, 128 / G))
         return THINK_ERR_CUDA;
     if (!ensure_smem(reinterpret_cast<const void *>(&paged_tc_kernel), paged_tc_smem())) return THINK_ERR_CUDA;
-    return launch_pdl(paged_tc_kernel, dim3(kTargetSMs), dim3(kPtThreads), paged_tc_smem(), st, mk, mv, mq, a, ok, ov, chunk, tma_q);
+    return launch_pdl(paged_tc_kernel, dim3(kTargetSMs), dim3(kPtThreads), paged_tc_smem(), st, mk, mv, mq, a, ks.outer(), vs.outer(), chunk, tma_q);
 }
 
 think_status_t launch_paged_tc32(const PagedArgs &a, cudaStream_t st)

@@ -300,6 +300,19 @@ def test_attn_pages_and_heads_at_any_distance(dtype, pad_page, pad_head):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("Hkv", [1, 2])
+def test_attn_pool_of_one_page(dtype, Hkv):
+    x = P.Batch([2], [10], 2 * Hkv, Hkv, 16, dtype, 43)
+    page = x.table[0][0]
+    w = attn_ws(x.T, 2 * Hkv, Hkv, dtype)
+    out = torch.full((x.T, 2 * Hkv, 128), 9.0, dtype=dtype, device="cuda")
+    qdk.think_paged_attn(x.q.cuda(), x.cache(x.k)[page:page + 1], x.cache(x.v)[page:page + 1],
+                         i32([[0] + x.table[0][1:]]), i32(x.q_start), i32(x.lens), out, w, scale=SCALE)
+    assert qdk.think_read_device_status(w) == 0
+    assert torch.equal(out, run_attn(x, 2 * Hkv, Hkv))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_attn_bad_pages_count_as_zeros(dtype):
     x = P.Batch([5, 40], [200, 90], 4, 2, 32, dtype, 9, poison=False)
     x.table[0][2], x.table[1][1] = -1, x.k.shape[0]

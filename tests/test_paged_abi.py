@@ -99,6 +99,16 @@ def test_paged_attn_refusals():
     assert f(B=0) == OK and f(T=0) == OK and f(Hkv=0) == OK
 
 
+def test_paged_attn_refuses_pools_that_no_step_divides():
+    ws = qdk.think_paged_attn_workspace_size(10, 4, 2)
+    f = caller(lib.think_paged_attn, q=FAKE, qs=i64(4096, 128), k=FAKE, ks=i64(4096, 2048, 128), v=FAKE, vs=i64(4096, 2048, 128),
+               pages=3, page=16, table=FAKE, ld=8, blocks=8, q_start=FAKE, lens=FAKE, B=2, T=10, max_new=0, Hq=4, Hkv=2, d=128,
+               dtype=qdk.THINK_BF16, scale=0.1, window=0, out=FAKE, os=i64(4096, 128), ws=FAKE, bytes=ws)
+    for name in ("ks", "vs"):
+        assert f(**{name: i64(1 << 38, 24, 128)}) == UNSUP and f(**{name: i64(24, 1 << 38, 128)}) == UNSUP, name
+        assert f(**{name: i64(4096, 2048, 1 << 36)}) == UNSUP, name  # eight rows apart by 2^40 bytes
+
+
 def test_gather_refusals():
     three = i64(4096, 2048, 128)
     f = caller(lib.think_gather_pages, c=FAKE, cs=three, pages=3, page=16, table=FAKE, ld=8, blocks=8, lens=FAKE, B=2, Hkv=2,
