@@ -116,17 +116,40 @@ think_status_t launch_paged_tc32(const PagedArgs &a, cudaStream_t st)
     return launch_pdl(paged_tc32_kernel, dim3(kTargetSMs), dim3(kP32Threads), kP32Smem, st, a);
 }
 
-template <typename T, bool NEIGHBOURS>
-think_status_t launch_rope_n(const RopeArgs &a, cudaStream_t st)
+template <typename T, bool NEIGHBOURS, int SLOTS, bool SHARED>
+think_status_t launch_rope_s(const RopeArgs &a, int64_t shares, int64_t blocks, cudaStream_t st)
 {
-    // a block holds up to 4 head rows a group of 16 (bf16) or 32 (fp32) lanes; more heads are shared between blocks
     const int groups = kRopeThreads * 16 / (kD * (int)sizeof(T));
-    const int64_t rows = a.Hq + 2 * (int64_t)a.Hkv, shares = ceil_div(rows, groups * kRopeUnroll);
-    const size_t smem = (size_t)kRopeStages * (size_t)ceil_div(ceil_div(rows, shares), groups) * kRopeThreads * 16;
-    auto kern = norm_rope_append_kernel<T, NEIGHBOURS>;
+    const int64_t rows = ceil_div(a.Hq + 2 * (int64_t)a.Hkv, shares) * a.unit;
+    const size_t smem = (size_t)kRopeStages * (size_t)ceil_div(rows, groups) * kRopeThreads * 16;
+    auto kern = norm_rope_append_kernel<T, NEIGHBOURS, SLOTS, SHARED>;
     if (!ensure_smem(reinterpret_cast<const void *>(kern), smem)) return THINK_ERR_CUDA;
-    const int64_t blocks = std::min(a.T, std::max<int64_t>(1, kTargetSMs * kRopeBlocksPerSM / shares));
     return launch_pdl(kern, dim3((unsigned)blocks, (unsigned)shares), dim3(kRopeThreads), smem, st, a);
+}
+
+template <typename T, bool NEIGHBOURS>
+think_status_t launch_rope_n(RopeArgs a, cudaStream_t st)
+{
+    // A group of 16 (bf16) or 32 (fp32) lanes takes up to three head rows of a token, and blocks share the heads so
+    // that a block's tokens times (its rows a group, and a half for the factors, which each forms) are fewest: three
+    // for many tokens (8192 of 48 bf16 heads: 41.5 us, two 43.7), one for few, which are then spread over the blocks.
+    // With few heads and many tokens a step takes as many tokens as fill one place, or two.
+    const int groups = kRopeThreads * 16 / (kD * (int)sizeof(T));
+    const int64_t heads = a.Hq + 2 * (int64_t)a.Hkv;
+    int64_t shares = 1, most = 1, least = INT64_MAX;
+    for (int s = 3; s > 0; --s) {
+        const int64_t n = ceil_div(heads, s * groups), x = std::max<int64_t>(1, kTargetSMs * kRopeBlocksPerSM / n);
+        const int64_t cost = ceil_div(a.T, x) * (2 * ceil_div(ceil_div(heads, n), groups) + 1);
+        if (cost < least) least = cost, shares = n, most = x;
+    }
+    const auto places = [&](int64_t unit) { return ceil_div(heads * unit, groups); };
+    a.unit = 1;
+    for (int u = 2; u <= kRopeBatch && places(u) <= 2 && u * most <= a.T; u *= 2)
+        if (u * places(a.unit) > a.unit * places(u)) a.unit = u;
+    const int64_t blocks = std::min(a.T, most);
+    if (a.unit > 1) return launch_rope_s<T, NEIGHBOURS, 2, true>(a, shares, blocks, st);
+    if (ceil_div(heads, shares) > 2 * groups) return launch_rope_s<T, NEIGHBOURS, 3, false>(a, shares, blocks, st);
+    return launch_rope_s<T, NEIGHBOURS, 2, false>(a, shares, blocks, st);
 }
 
 template <typename T>

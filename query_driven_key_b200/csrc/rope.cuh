@@ -20,21 +20,23 @@
 // all heads of a token share them).  The angle is formed and reduced in fp64:
 // at position 131072 an fp32 product is off by up to 2^-24 * 131072 = 0.008 rad.
 // All arithmetic after it is fp32, with one rounding at the store.
-// Measured: 8192 tokens of 32 + 8 + 8 bf16 heads (201 MB) 42.9 us = 4.7 TB/s;
-// 1777 tokens of 12 + 4 + 4 fp32 heads (36 MB) 8.8 us; one token 3.6 us.  Rows
-// held in registers instead of the ring (90 a thread, two blocks an SM) 90, the
-// ring without fixed heads a thread 65, with three blocks of fewer threads 44.
+// Measured: 8192 tokens of 32 + 8 + 8 bf16 heads (201 MB) 42.1 us = 4.8 TB/s;
+// 1777 tokens of 12 + 4 + 4 fp32 heads (36 MB) 8.4 us; one token 3.5 us.  Bound by
+// the issue of instructions (147 for two rows of a warp, 0.64 of the issue slots)
+// beside HBM: what helps is fewer idle lanes.  512 threads of two rows each 43.3
+// (48 rows are one and a half a thread group); rows held in registers instead
+// of the ring (90 a thread, two blocks an SM) 90; the ring without fixed heads a
+// thread 65.
 #pragma once
 
 #include "ptx.cuh"
 
 namespace think {
 
-constexpr int kRopeThreads = 512;
-constexpr int kRopeUnroll = 2;       // head rows of a thread
-constexpr int kRopeStages = 4;       // tokens in shared memory
+constexpr int kRopeThreads = 256;
+constexpr int kRopeStages = 3;       // steps in shared memory (four blocks an SM)
 constexpr int kRopeBatch = kRopeThreads / (kD / 2);  // tokens whose factors are formed together
-constexpr int kRopeBlocksPerSM = 2;
+constexpr int kRopeBlocksPerSM = 4;
 
 struct RopeArgs {
     const void *q, *k, *v, *wq, *wk;
@@ -46,6 +48,7 @@ struct RopeArgs {
     int64_t kc_sp, kc_sh, kc_sn, vc_sp, vc_sh, vc_sn;
     int64_t num_slots, T;
     int Hq, Hkv, rot, page_size;
+    int unit;  // tokens of a step, a power of two up to kRopeBatch
     float eps;
 };
 
@@ -118,10 +121,13 @@ template <> struct RopeChunk<float> {
     }
 };
 
-// Rows of a block: blockIdx.y's share of the q, k and v heads (at most UNIT),
+// Rows of a block: blockIdx.y's share of the q, k and v heads (at most SLOTS a thread group),
 // of the tokens [T x / X, T (x + 1) / X), x = blockIdx.x of X.  Row slot i of a
 // thread is a fixed head, so that its addresses only move with the token.
-template <typename T, bool NEIGHBOURS>
+// SHARED: few heads; a step takes a.unit tokens (else one), whose rows, one after
+// another, fill the row slots (8192 tokens of 1 + 1 + 1 bf16 heads 10.9 us, a token a
+// step 22.7).
+template <typename T, bool NEIGHBOURS, int SLOTS, bool SHARED>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSM) norm_rope_append_kernel(const RopeArgs a)
 {
     constexpr int CH = RopeChunk<T>::N;           // channels of a chunk
@@ -138,27 +144,31 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSM) norm_rope_appe
     const int rows = a.Hq + 2 * a.Hkv, half = a.rot / 2;
     const int row0 = (int)((int64_t)rows * blockIdx.y / gridDim.y), row1 = (int)((int64_t)rows * (blockIdx.y + 1) / gridDim.y);
     const int64_t t0 = a.T * blockIdx.x / gridDim.x, t1 = a.T * (blockIdx.x + 1) / gridDim.x;
-    const uint32_t stage_bytes = (uint32_t)((row1 - row0 + GROUPS - 1) / GROUPS) * (kRopeThreads * 16);
+    const int U = SHARED ? a.unit : 1;
+    const uint32_t stage_bytes = (uint32_t)(((row1 - row0) * U + GROUPS - 1) / GROUPS) * (kRopeThreads * 16);
     // This lane's chunks: channels a0 .. and b0 .., each the other's partners
     // (NEIGHBOURS: partners lie beside each other); lanes past the turned
     // channels hold neighbouring chunks of the rest.
     const int turning = NEIGHBOURS ? 0 : half / CH;
     const int a0 = NEIGHBOURS ? lane * VEC : lane < turning ? lane * CH : a.rot + (lane - turning) * VEC;
     const int b0 = !NEIGHBOURS && lane < turning ? a0 + half : a0 + CH;
-    const unsigned char *src[kRopeUnroll];  // the next token's vector of this thread
-    int64_t step[kRopeUnroll];              // bytes to the token after it
-    T *dst[kRopeUnroll];                    // the head's row but for s_off
-    int kind[kRopeUnroll];                  // 0 q, 1 k, 2 v, 3 none
+    const unsigned char *src[SLOTS];  // the next step's vector of this thread
+    int64_t step[SLOTS];              // bytes to the step after it
+    T *dst[SLOTS];                    // the head's row but for s_off
+    int kind[SLOTS];                  // 0 q, 1 k, 2 v, 3 none
+    int tok[SLOTS];                   // token of the step
 #pragma unroll
-    for (int i = 0; i < kRopeUnroll; ++i) {
-        const int r = row0 + grp + i * GROUPS;
-        kind[i] = r >= row1 ? 3 : r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;
+    for (int i = 0; i < SLOTS; ++i) {
+        const int at = grp + i * GROUPS;
+        tok[i] = SHARED ? min(at / (row1 - row0), U) : at >= row1 - row0 ? 1 : 0;
+        const int r = row0 + at - tok[i] * (row1 - row0);
+        kind[i] = tok[i] == U ? 3 : r < a.Hq ? 0 : r < a.Hq + a.Hkv ? 1 : 2;
         const int h = r - (kind[i] == 0 ? 0 : kind[i] == 1 ? a.Hq : a.Hq + a.Hkv);
         const void *p = kind[i] == 0 ? a.q : kind[i] == 1 ? a.k : a.v;
         const int64_t st = kind[i] == 0 ? a.q_st : kind[i] == 1 ? a.k_st : a.v_st;
         const int64_t sh = kind[i] == 0 ? a.q_sh : kind[i] == 1 ? a.k_sh : a.v_sh;
-        step[i] = st * (int64_t)sizeof(T);
-        src[i] = kind[i] == 3 ? nullptr : static_cast<const unsigned char *>(p) + t0 * step[i] + (h * sh + lane * VEC) * (int64_t)sizeof(T);
+        step[i] = U * st * (int64_t)sizeof(T);
+        src[i] = kind[i] == 3 ? nullptr : static_cast<const unsigned char *>(p) + ((t0 + tok[i]) * st + h * sh + lane * VEC) * (int64_t)sizeof(T);
         dst[i] = kind[i] == 0   ? static_cast<T *>(a.q_out) + h * a.qo_sh
                  : kind[i] == 1 ? static_cast<T *>(a.k_cache) + h * a.kc_sh
                                 : static_cast<T *>(a.v_cache) + h * a.vc_sh + lane * VEC;
@@ -168,14 +178,15 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSM) norm_rope_appe
     int ahead = (int)(t1 - t0);  // tokens not yet fetched
     uint32_t fs = 0;             // stage of the next one
     auto fetch = [&]() {
-        if (ahead-- > 0) {
+        if (ahead > 0) {
             const uint32_t to = smem_addr(ring) + fs + tid * 16;
 #pragma unroll
-            for (int i = 0; i < kRopeUnroll; ++i)
-                if (kind[i] != 3) {
+            for (int i = 0; i < SLOTS; ++i)
+                if (SHARED ? tok[i] < min(ahead, U) : tok[i] == 0) {
                     cp_async_16(to + i * (kRopeThreads * 16), src[i]);
                     src[i] += step[i];
                 }
+            ahead -= U;
         }
         cp_async_commit();
         fs = fs == (kRopeStages - 1) * stage_bytes ? 0 : fs + stage_bytes;
@@ -243,13 +254,15 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSM) norm_rope_appe
         }
         __syncthreads();
         const int n = (int)min((int64_t)kRopeBatch, t1 - first);
-        for (int k = 0; k < n; ++k) {
+        for (int k0 = 0; k0 < n; k0 += U) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kRopeStages - 2) : "memory");
             __syncwarp();  // the warp's lanes share its rows
             const unsigned char *held_rows = ring + stage + (uint32_t)grp * (kD * sizeof(T));
 #pragma unroll
-            for (int i = 0; i < kRopeUnroll; ++i) {
-                if (row0 + i * GROUPS >= row1) break;
+            for (int i = 0; i < SLOTS; ++i) {
+                if (i * GROUPS >= (row1 - row0) * U) break;
+                const int k = k0 + (SHARED ? tok[i] : 0);
+                if (SHARED && k >= n) continue;
                 const unsigned char *row = held_rows + i * (kRopeThreads * 16);
                 if (kind[i] >= 2) {  // a value row: as it is
                     if (kind[i] == 2 && s_off[k][2] >= 0)

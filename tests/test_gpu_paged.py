@@ -130,7 +130,10 @@ def rope_case(T, Hq, Hkv, dtype, rot, neighbours, norm, page, layout, seed, far=
     (37, 6, 2, BF, 96, False, True, 48, "nhd"), (37, 6, 2, BF, 96, True, False, 48, "nhd"),
     (130, 40, 40, BF, 64, False, False, 64, "hnd"), (19, 3, 1, F32, 16, False, True, 32, "nhd"),
     (64, 71, 3, F32, 128, False, True, 16, "hnd"), (5, 4, 2, BF, 0, False, True, 16, "hnd"),
-    (9, 4, 2, F32, 0, True, False, 16, "hnd"), (11, 16, 1, BF, 32, True, True, 128, "hnd")])
+    (9, 4, 2, F32, 0, True, False, 16, "hnd"), (11, 16, 1, BF, 32, True, True, 128, "hnd"),
+    # several tokens a step (a block's tokens no multiple of them), and three head rows a thread group
+    (2600, 1, 1, BF, 128, False, True, 64, "hnd"), (1301, 4, 2, F32, 128, True, True, 16, "nhd"), (603, 8, 4, BF, 64, True, True, 32, "hnd"),
+    (600, 6, 1, F32, 96, False, True, 16, "hnd"), (310, 64, 8, BF, 128, False, True, 16, "hnd"), (19, 32, 8, F32, 128, True, True, 48, "nhd")])
 def test_norm_rope_append(T, Hq, Hkv, dtype, rot, neighbours, norm, page, layout):
     eps = 1e-6
     q, k, v, wq, wk, freq, positions, slots, (kc, vc) = rope_case(T, Hq, Hkv, dtype, rot, neighbours, norm, page, layout, T + rot)
