@@ -228,6 +228,15 @@ def test_attn(i, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("new,ctx", [
+    ([1] * 12, [128 * n + d for n in (15, 16, 17) for d in (-2, -1, 0, 1)]),  # single tokens about 16 key tiles
+    ([64, 33, 65, 130], [128 * 15, 128 * 16, 900, 1000]), ([70] * 6, [128 * 7, 128 * 7 + 58, 128 * 8, 1200, 60, 0]),
+    ([1], [128 * 17]), ([1, 1, 400], [128 * 16 + 1, 5, 600])])
+def test_attn_short_items_and_those_that_are_cut(new, ctx, dtype):
+    check_attn(P.Batch(new, ctx, 8, 2, 32, dtype, 77 + len(new)), 8, 2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_attn_rows_that_see_nothing(dtype):
     """Fewer tokens cached than new ones: the first rows have positions below 0 and get zeros."""
     x = P.Batch([6, 300, 4], [0, 0, 0], 4, 2, 16, dtype, 3, lens=[2, 170, 0])
