@@ -7,15 +7,20 @@
 // it, is
 //     x0 y2 + x2 y0 + x1 y1 + x0 y1 + x1 y0 + x0 y0,
 // six bf16 products with fp32 sums, added from the smallest on.  The tensor
-// core's sums lose up to a unit of the last place a step, towards zero: the small
-// terms of O have an accumulator of their own, so that O itself takes 4 steps a
-// tile and not 24 (error of 400 rows over 2400 keys against 64 bits 1.3e-6 with
-// one accumulator).  Both products
+// core's sums drop what is below their last place, up to two units a step and
+// always towards zero, so that a sum over a long item would lose in
+// proportion to its steps (1.6e-4 over 40000 keys of one sign in one block).  A
+// tile's O is therefore a sum of its own, of 4 steps with the large terms, and
+// the softmax threads add it, rounded to nearest, to the item's O in another part
+// of TMEM, beside the next logits' products: 6e-7 over those 40000 keys, 3e-7 over
+// 131072 keys of 8 heads shared by all blocks (plain fp32: 2e-7 to 1.5e-6), for
+// 4% of the time there and none for short chunks.  Both products
 // of the attention are formed that way, at a sixth of the bf16
 // rate, which is several times the rate of the FMA pipes:
 //     S = Q K^T      128 query rows x 64 keys; the parts of Q, K in shared memory
 //     P = 2^(s S - m) and its three parts: one thread a row, to TMEM
-//     O += P V       the parts of P in TMEM, those of V in shared memory
+//     O_j = P V      the parts of P in TMEM, those of V in shared memory
+//     O = f (O + O_j)    f: 2^(old m - new m)
 // with the running reference m and sum l as in the bf16 kernel (m follows the
 // maximum when that has grown by more than 2^kPtLazy).
 //
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
     tc05::fence_before_sync();
     __syncthreads();
     tc05::fence_after_sync();
-    const uint32_t tmem = bars.tmem;  // S 0 .. 127 (two buffers), O 128 .. 255, P 256 .. 351 (three parts), small terms of O 352 .. 479
+    const uint32_t tmem = bars.tmem;  // S 0 .. 127 (two buffers), a tile's O 128 .. 255, P 256 .. 351 (three parts), the item's O 352 .. 479
     bool ok = true;
     auto wait = [&](uint32_t bar, uint32_t phase) {  // false from the first wait that runs out on
         if (ok) ok = pt_wait(bar, phase & 1, abort_flag, a.status, THINK_DEVICE_TIMEOUT_FULL);
@@ -161,15 +166,14 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
                 if (!wait(p_full, nv)) break;
                 ++nv;
                 tc05::fence_after_sync();
-                const bool more = uniform(j > 0) != 0;
-                if (leader) {  // O (+)= P V_j
+                if (leader) {  // O = P V_j
 #pragma unroll
                     for (int i = 0; i < 6; ++i)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            tc05::mma_bf16_ts(tmem + (i < 5 ? 352u : 128u), tmem + 256u + 32u * term_left(i) + 8u * k,
+                            tc05::mma_bf16_ts(tmem + 128u, tmem + 256u + 32u * term_left(i) + 8u * k,
                                               v_desc + (((uint32_t)term_right(i) * kP32KPart + 2048u * k) >> 4), idesc_o,
-                                              more || (i > 0 && i < 5) || k > 0);
+                                              i > 0 || k > 0);
                     tc05::commit(pv_done);
                 }
             }
@@ -261,7 +265,7 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
     } else {
         // ----------------------------------------------------------- softmax
         const uint32_t lane_addr = tmem + ((uint32_t)(32 * warp) << 16), o_addr = lane_addr + 128u, p_addr = lane_addr + 256u,
-                       low_addr = lane_addr + 352u;
+                       sum_addr = lane_addr + 352u;
         const float sl = fmaxf(fabsf(a.scale_log2), 1.0e-30f);  // a scale of 0 still sends -inf to -inf
         uint32_t g = 0;  // tiles of the part
         for (W w(a, plan_sm, parts, part); w.live(); w.next()) {
@@ -273,6 +277,20 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
             const int pos = w.s.kv - w.s.n + (real ? tok : w.s.n - 1);
             if (!w.whole && tid == 0) find_pieces(pieces, parts, w);
             float m = -INFINITY, l = 0.f;
+            // channels 16 i .. of O: the last tile's, added to those of the tiles before where there are any
+            auto item_o = [&](int i, bool more, uint32_t (&o)[16]) {
+                tc05::tmem_ld16_issue(o_addr + 16u * i, o);
+                if (more) {
+                    uint32_t x[16];
+                    tc05::tmem_ld16_issue(sum_addr + 16u * i, x);
+                    tc05::tmem_ld_wait(x);
+                    tc05::tmem_ld_wait(o);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(x[c]));
+                } else {
+                    tc05::tmem_ld_wait(o);
+                }
+            };
             for (int jt = w.j0; jt < w.j1; ++jt, ++g) {
                 wait(s_full + 8 * (g & 1), g >> 1);
                 if (warp_real) {
@@ -312,18 +330,6 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
                     l += (s[0] + s[1]) + (s[2] + s[3]);
                     if (g > 0) wait(pv_done, g - 1);  // P and O are free
                     tc05::fence_after_sync();
-                    if (jt > w.j0 && __any_sync(0xffffffffu, grow)) {
-#pragma unroll 1
-                        for (int i = 0; i < 16; ++i) {
-                            const uint32_t at16 = (i < 8 ? o_addr : low_addr) + 16u * (i & 7);
-                            uint32_t o[16];
-                            tc05::tmem_ld16_issue(at16, o);
-                            tc05::tmem_ld_wait(o);
-#pragma unroll
-                            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
-                            tc05::tmem_st16(at16, o);
-                        }
-                    }
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         uint32_t p[3][16];
@@ -335,6 +341,16 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
                         }
 #pragma unroll
                         for (int k = 0; k < 3; ++k) tc05::tmem_st16(p_addr + 32u * k + 16u * i, p[k]);
+                    }
+                    if (jt > w.j0) {  // the tile before: its O joins the item's, on the new reference
+#pragma unroll 1
+                        for (int i = 0; i < 8; ++i) {
+                            uint32_t o[16];
+                            item_o(i, jt - 1 > w.j0, o);
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+                            tc05::tmem_st16(sum_addr + 16u * i, o);
+                        }
                     }
                     tc05::tmem_st_wait();
                     tc05::fence_before_sync();
@@ -352,24 +368,19 @@ __global__ void __launch_bounds__(kP32Threads, 1) paged_tc32_kernel(const PagedA
                              (int64_t)(w.p.h * a.group.d + row - tok * a.group.d) * a.o_sh;
                 float *pt = part_at(a, part, w.head ? 1 : 0, 0) + tid;  // element x of the row at pt[x * rows_cap]
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t o[32], low[32];
-                    tc05::tmem_ld32_issue(o_addr + 32u * i, o);
-                    tc05::tmem_ld32_issue(low_addr + 32u * i, low);
-                    tc05::tmem_ld32_wait(o);
-                    tc05::tmem_ld32_keep(low);
+                for (int i = 0; i < 8; ++i) {
+                    uint32_t o[16];
+                    item_o(i, w.j1 - w.j0 > 1, o);
                     if (!real) continue;
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) + __uint_as_float(low[c]));
                     if (w.whole) {
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4)
-                            *reinterpret_cast<float4 *>(dst + 32 * i + c) =
+                        for (int c = 0; c < 16; c += 4)
+                            *reinterpret_cast<float4 *>(dst + 16 * i + c) =
                                 make_float4(__uint_as_float(o[c]) * inv, __uint_as_float(o[c + 1]) * inv,
                                             __uint_as_float(o[c + 2]) * inv, __uint_as_float(o[c + 3]) * inv);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) pt[(32 * i + c) * a.rows_cap] = __uint_as_float(o[c]);
+                        for (int c = 0; c < 16; ++c) pt[(16 * i + c) * a.rows_cap] = __uint_as_float(o[c]);
                     }
                 }
                 if (real && !w.whole) pt[kD * a.rows_cap] = m * sl, pt[(kD + 1) * a.rows_cap] = l;

@@ -1,0 +1,74 @@
+"""The attention over pages on the GPU, held to the bounds of paged_bounds."""
+import math
+
+import pytest
+import torch
+
+import paged_bounds as Q
+
+pytestmark = pytest.mark.gpu
+qdk = pytest.importorskip("query_driven_key_b200")
+
+BF, F32, F64 = torch.bfloat16, torch.float32, torch.float64
+SCALE = 1.0 / math.sqrt(128.0)
+
+
+def attend(q, k, v, table, q_start, lens, window=0, scale=SCALE):
+    """think_paged_attn on CPU or GPU tensors, lists for the integers; the status word has to be 0."""
+    i32 = lambda x: torch.as_tensor(x, dtype=torch.int32).cuda()
+    q, k, v = q.cuda(), k.cuda(), v.cuda()
+    T, Hq, _ = q.shape
+    w = torch.zeros(qdk.think_paged_attn_workspace_size(T, Hq, k.shape[1], dtype=q.dtype), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, 9.0)
+    qdk.think_paged_attn(q, k, v, i32(table), i32(q_start), i32(lens), out, w, window=window, scale=scale)
+    assert qdk.think_read_device_status(w) == 0
+    return out
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("i", range(len(Q.LONG)))
+def test_long_contexts(i, dtype):
+    Hq, Hkv, window = Q.LONG[i][2], Q.LONG[i][3], Q.LONG[i][5]
+    x = Q.long_batch(i, dtype)
+    want, size, spread, logit = Q.exact(x, SCALE)
+    limit = Q.bound(want, size, spread, logit, dtype, Q.chain(x, Hq, Hkv))
+    got = attend(x.q, x.cache(x.k), x.cache(x.v), x.table, x.q_start, x.lens, window).cpu().to(F64)
+    assert ((got - want).abs() / limit).max().item() <= 1.0
+
+
+@pytest.mark.parametrize("keys", [3000, 20000])
+def test_fp32_mean_of_positive_values(keys):
+    """Nearly equal weights over one long item a block: what the sums of O drop would all have one sign."""
+    B, page = Q.PARTS, 64
+    cols = -(-keys // page)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    v = torch.rand((B * cols, 1, page, 128), generator=g, device="cuda") + 0.5
+    k = torch.randn((B * cols, 1, page, 128), generator=g, device="cuda")
+    table = torch.randperm(B * cols, generator=g, device="cuda").reshape(B, cols)
+    q = 0.01 * torch.randn((B, 1, 128), generator=g, device="cuda")
+    got = attend(q, k, v, table, list(range(B + 1)), [keys] * B).to(F64)
+    for b in range(B):
+        kk, vv = (c[table[b], 0].reshape(-1, 128)[:keys].to(F64) for c in (k, v))
+        want = torch.softmax(SCALE * (q[b].to(F64) @ kk.T), -1) @ vv
+        limit = Q.mean_bound(-(-keys // 64), SCALE * (q[b].to(F64).abs() @ kk.abs().T).max().item())
+        assert ((got[b] - want).abs() / want).max().item() <= limit, b
+
+
+def test_fp32_values_keep_their_third_part():
+    v = Q.with_third_part((1 + torch.rand((3, 1, 512, 128), generator=torch.Generator().manual_seed(2)) / 2).to(BF))
+    v[:] = v[:, :, :1]  # every row the same: the mean is the row
+    k = torch.randn(v.shape, generator=torch.Generator().manual_seed(4))
+    got = attend(torch.zeros(1, 1, 128), k, v[:1].expand(3, -1, -1, -1).contiguous(), [[2, 0, 1]], [0, 1], [1200]).cpu().to(F64)
+    want = v[0, 0, 0].to(F64)
+    assert ((got[0, 0] - want).abs() / want).max().item() <= Q.mean_bound(20)
+
+
+def test_fp32_logits_keep_their_third_parts():
+    q, k0 = Q.two_key_case()
+    B = len(q)
+    qq, k, v = torch.zeros(B, 1, 128), torch.zeros(B, 1, 16, 128), torch.zeros(B, 1, 16, 128)
+    qq[:, 0, 5], k[:, 0, 0, 5] = q, k0
+    v[:, 0, 0], v[:, 0, 1] = 1.0, -1.0
+    got = attend(qq, k, v, [[b] for b in range(B)], list(range(B + 1)), [2] * B, scale=1.0).cpu().to(F64)
+    want, limit = Q.two_key_want(q, k0), Q.two_key_bound(q, k0)
+    assert ((got[:, 0] - want[:, None]).abs() / limit[:, None]).max().item() <= 1.0
