@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+#include <map>
 #include <mutex>
 #include <utility>
 
@@ -188,27 +189,22 @@ void map_cache_put(const MapKey &k, const CUtensorMap &m)
     e.used = true;
 }
 
-// cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel, device
-// and size (per thread; the attribute itself is per device).
+// Allow a kernel `bytes` of dynamic shared memory.  The attribute belongs to the
+// kernel and the device, whichever thread sets it, so that the sizes are kept for
+// the process and only ever raised: a call that needs less must not take away
+// what another thread's next launch of the same kernel relies on.
 bool ensure_smem(const void *kern, size_t bytes)
 {
-    struct Entry {
-        const void *kern;
-        int dev;
-        size_t bytes;
-    };
-    thread_local Entry seen[64];
-    thread_local int nseen = 0;
+    static std::mutex mutex;
+    static std::map<std::pair<const void *, int>, size_t> allowed;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    for (int i = 0; i < nseen; ++i)
-        if (seen[i].kern == kern && seen[i].dev == dev && seen[i].bytes >= bytes) return true;
+    const std::lock_guard<std::mutex> lock(mutex);
+    size_t &have = allowed[{kern, dev}];
+    if (have >= bytes) return true;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
         return false;
-    Entry &e = seen[nseen < 64 ? nseen++ : (int)(reinterpret_cast<uintptr_t>(kern) >> 4) % 64];
-    e.kern = kern;
-    e.dev = dev;
-    e.bytes = bytes;
+    have = bytes;
     return true;
 }
 
