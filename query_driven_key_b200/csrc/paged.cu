@@ -106,8 +106,12 @@ think_status_t launch_paged_tc(const PagedArgs &a, cudaStream_t st)
     if (!tma_q) mq = mk;
     else if (!make_map_4d(&mq, THINK_BF16, a.q, kD, Hq, a.T, 1, Hq > 1 ? a.q_sh : kD, a.T > 1 ? a.q_st : kD, kD, 64, G, true, 128 / G))
         return THINK_ERR_CUDA;
-    if (!ensure_smem(reinterpret_cast<const void *>(&paged_tc_kernel), paged_tc_smem())) return THINK_ERR_CUDA;
-    return launch_pdl(paged_tc_kernel, dim3(kTargetSMs), dim3(kPtThreads), paged_tc_smem(), st, mk, mv, mq, a, ks.outer(), vs.outer(), chunk, tma_q);
+    // the most key tiles of an item that a block can have: an item's, or an equal share of all items' and what is not cut
+    const int64_t tiles = ceil_div(a.limit, kPtBN), items = a.Hkv * (ceil_div((int64_t)a.T * G, kPtRows) + a.B);
+    const bool is_long = std::min(tiles, items * (tiles + kItemCost<kPtRows>) / kTargetSMs + 17) > kPtFold;
+    const auto kern = is_long ? paged_tc_kernel<true> : paged_tc_kernel<false>;
+    if (!ensure_smem(reinterpret_cast<const void *>(kern), paged_tc_smem())) return THINK_ERR_CUDA;
+    return launch_pdl(kern, dim3(kTargetSMs), dim3(kPtThreads), paged_tc_smem(), st, mk, mv, mq, a, ks.outer(), vs.outer(), chunk, tma_q);
 }
 
 think_status_t launch_paged_tc32(const PagedArgs &a, cudaStream_t st)

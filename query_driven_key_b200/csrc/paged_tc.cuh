@@ -59,6 +59,7 @@ constexpr int kPtMma = 9;
 constexpr int kPtStages = 5;
 constexpr uint32_t kPtTile = 32768u;
 constexpr float kPtLazy = 8.f;
+constexpr int kPtFold = 256;  // key tiles of a warpgroup after which its O moves on
 constexpr int kPtEarly = 96;  // keys of a tile whose P is handed over while the rest's is formed
 
 struct PtBars {
@@ -197,6 +198,10 @@ struct PtOuter {
     int page, head, none;
 };
 
+// LONG: a block may have so many tiles of one item that its O has to move on (see
+// there).  Its code costs the calls that cannot 1 to 2.5% (prompt of 16384
+// tokens 1999 -> 2031 us, 131072 keys 100.5 -> 103.0), so that it is a variant.
+template <bool LONG>
 __global__ void __launch_bounds__(kPtThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ CUtensorMap tm_q, const PagedArgs a, const PtOuter outer_k,
@@ -509,7 +514,35 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (!w.whole && tid == 0) find_pieces(pieces, parts, w);
             float m = -INFINITY, l = 0.f;
             const int step = x.split ? 2 : 1, j0 = x.split ? t : 0;
+            // The tensor core's sums drop what is below their last place, always towards zero: over 200000 keys of one
+            // item a sum of values of one sign lost 8e-4 to 1.2e-3.  So every kPtFold tiles O moves on: it is added, rounded
+            // to nearest, to what moved on before, in the place of this piece's partial, and starts from zero; at
+            // the item's end it comes back (to_end).  2.5e-4 at any length, a sixteenth of the output's half step.
+            auto move = [&](bool before, bool to_end) {
+                tc05::fence_after_sync();
+                float *y = part_at(a, part, w.head ? 1 : 0, t) + r;  // element c of the row at y[c * rows_cap]
+                const float m_moved = before && real ? y[kD * a.rows_cap] : -INFINITY;
+                const float f = m_moved == -INFINITY ? 0.f : exp2_approx((m_moved - m) * sl);
+                if (real && !to_end) y[kD * a.rows_cap] = m;
+#pragma unroll 1
+                for (int i = 0; i < 16; ++i, y += 8 * a.rows_cap) {
+                    uint32_t o[8];
+                    tc05::tmem_ld8(o_addr + 8u * i, o);
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        if (f != 0.f) o[c] = __float_as_uint(__uint_as_float(o[c]) + f * y[c * a.rows_cap]);
+                        if (real && !to_end) y[c * a.rows_cap] = __uint_as_float(o[c]);
+                        if (!to_end) o[c] = 0u;
+                    }
+                    tc05::tmem_st8(o_addr + 8u * i, o);
+                }
+                tc05::tmem_st_wait();
+            };
             for (int j = j0; j < x.n; j += step) {
+                if (LONG && j >= kPtFold * step && (j & (kPtFold * step - 1)) == j0) {
+                    wait(sfull0 + 8 * t, ns);  // (of the tile to come: the products before it are done)
+                    if (warp_real) move(j >= 2 * kPtFold * step, false);
+                }
                 wait(sfull0 + 8 * t, ns++);
                 if (warp_real) {
                     tc05::fence_after_sync();
@@ -615,6 +648,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (!late) next_q();
             if (any) wait(ofull0 + 8 * t, no++);
             tc05::fence_after_sync();
+            if (LONG && x.n > kPtFold * step + j0 && warp_real) move(true, true);
             auto load_o = [&](int i, uint32_t (&o)[32]) {
                 if (any) {
                     tc05::tmem_ld32_issue(o_addr + 32u * i, o);

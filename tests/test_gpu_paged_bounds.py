@@ -54,6 +54,28 @@ def test_fp32_mean_of_positive_values(keys):
         assert ((got[b] - want).abs() / want).max().item() <= limit, b
 
 
+@pytest.mark.parametrize("B,G", [(148, 1), (100, 2), (148, 160)])
+def test_bf16_sums_over_long_items_do_not_drift(B, G):
+    """200000 keys a request and positive values: keys shared by the halves of a block, in one piece and cut, and rows
+    shared.  Of 8 * 256 steps between two roundings to nearest each drops at most 2 u; the mean over all outputs leaves
+    6 standard deviations of a rounding, 2^-8 / sqrt(3), of this result and of the exact one."""
+    keys, page, pool = 200000, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(B + G)
+    v = (torch.rand((pool, 1, page, 128), generator=g, device="cuda") + 0.5).to(BF)
+    k = torch.randn((pool, 1, page, 128), generator=g, device="cuda").to(BF)
+    q = torch.randn((B, G, 128), generator=g, device="cuda").to(BF)
+    table = torch.randint(0, pool, (B, keys // page), generator=g, device="cuda")
+    got = attend(q, k, v, table, list(range(B + 1)), [keys] * B).to(F64)
+    want = torch.empty_like(got)
+    for b in range(B):
+        e = torch.exp(SCALE * (q[b].to(F64) @ k.reshape(-1, 128).to(F64).T))
+        e = e * torch.bincount(table[b], minlength=pool).repeat_interleave(page)
+        want[b] = e @ v.reshape(-1, 128).to(F64) / e.sum(-1, keepdim=True)
+    drift = ((got - want.to(BF).to(F64)) / want).mean().item()
+    assert abs(drift) <= 8 * 256 * 2 * Q.U + 6 * 2.0 ** -8 / math.sqrt(3.0) * math.sqrt(2.0 / got.numel())
+    assert ((got - want).abs() <= (2.0 ** -8 + 2.0 ** -10) * want).all()
+
+
 def test_fp32_values_keep_their_third_part():
     v = Q.with_third_part((1 + torch.rand((3, 1, 512, 128), generator=torch.Generator().manual_seed(2)) / 2).to(BF))
     v[:] = v[:, :, :1]  # every row the same: the mean is the row
