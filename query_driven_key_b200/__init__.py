@@ -11,6 +11,7 @@ importing this package raises if ``libthink.so`` cannot be loaded.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.util
 import os
@@ -698,7 +699,11 @@ class PagedCache:
     tables of the current step.  Allocates with torch on construction, then
     only calls the C entry points (release moves a request's page numbers with
     torch).  A step: extend once, then append and attend in each layer; prune
-    hands a request over to the channel pruning."""
+    hands a request over to the channel pruning.
+
+    Every method works on `stream` (None: the device's current one), what it
+    allocates included; another stream than the one that the cache was made or
+    last used on has to wait for that one first."""
 
     def __init__(self, B: int, Hq: int, Hkv: int, num_pages: int, page_size: int, max_blocks: int, max_rows: int,
                  layers: int = 1, d: int = 128, dtype: torch.dtype = torch.bfloat16, device="cuda"):
@@ -738,24 +743,37 @@ class PagedCache:
 
     def gather(self, b: int, N: int, layer: int = 0, stream=None):
         """The first N tokens of request b, contiguous: k, v [1,Hkv,N,d]."""
-        out = [torch.empty((1, self.Hkv, N, self.d), dtype=self.dtype, device=self.kv_lens.device) for _ in range(2)]
-        for cache, o in zip((self.k_cache[layer], self.v_cache[layer]), out):
-            think_gather_pages(cache, self.block_table[b:b + 1], self.kv_lens[b:b + 1], o, stream)
+        with self._on(stream):
+            out = [torch.empty((1, self.Hkv, N, self.d), dtype=self.dtype, device=self.kv_lens.device) for _ in range(2)]
+            for cache, o in zip((self.k_cache[layer], self.v_cache[layer]), out):
+                think_gather_pages(cache, self.block_table[b:b + 1], self.kv_lens[b:b + 1], o)
         return out
 
     def prune(self, b: int, N: int, q_win, T: int, layer: int = 0, stream=None):
         """Request b, N tokens long, pruned to T key channels by its window queries q_win [1,Hq,S,d]: a PrunedCache and
         the values [1,Hkv,N,d] for its decode."""
-        k, v = self.gather(b, N, layer, stream)
-        pruned = PrunedCache(1, self.Hq, self.Hkv, N, T, self.d, dtype=self.dtype, device=k.device)
-        pruned.prune(q_win, k, stream)
+        with self._on(stream):
+            k, v = self.gather(b, N, layer)
+            pruned = PrunedCache(1, self.Hq, self.Hkv, N, T, self.d, dtype=self.dtype, device=k.device)
+            pruned.prune(q_win, k)
         return pruned, v
 
-    def release(self, b: int):
-        """Request b is done: its pages go back to the stack, its length to 0 (on the current stream)."""
-        j = torch.arange(self.max_blocks, device=self.kv_lens.device)
-        n = (self.kv_lens[b] + self.page_size - 1) // self.page_size
-        self._stack[torch.where(j < n, self.free_count + j, self.num_pages + j)] = self.block_table[b]
-        self.free_count += n
-        self.kv_lens[b] = 0
-        self.block_table[b] = -1
+    def release(self, b: int, stream=None):
+        """Request b is done: its pages go back to the stack, its length to 0."""
+        with self._on(stream):
+            j = torch.arange(self.max_blocks, device=self.kv_lens.device)
+            n = (self.kv_lens[b] + self.page_size - 1) // self.page_size
+            self._stack[torch.where(j < n, self.free_count + j, self.num_pages + j)] = self.block_table[b]
+            self.free_count += n
+            self.kv_lens[b] = 0
+            self.block_table[b] = -1
+
+    @contextlib.contextmanager
+    def _on(self, stream):
+        """This cache's device and `stream` current: allocations and fills are then in the stream's order, and memory
+        that is dropped goes to nothing but the stream's later work."""
+        device = self.kv_lens.device
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+        with torch.cuda.device(device), torch.cuda.stream(stream):
+            yield

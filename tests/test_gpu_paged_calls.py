@@ -32,3 +32,55 @@ def test_a_small_call_of_another_thread_does_not_take_shared_memory_away():
     assert not failed
     call(8192)
     torch.cuda.synchronize()
+
+
+def filled(lens, Hq=8, Hkv=2, dtype=BF, page=32, seed=0, **kw):
+    """A PagedCache with these lengths, the queries of its tokens and the inputs' keys and values."""
+    need = sum(-(-n // page) for n in lens)
+    cache = qdk.PagedCache(len(lens), Hq, Hkv, num_pages=need + 8, page_size=page, max_blocks=max(lens) // page + 4,
+                           max_rows=sum(lens), dtype=dtype, **kw)
+    g = torch.Generator().manual_seed(seed)
+    qkv = torch.randn((sum(lens), Hq + 2 * Hkv, 128), generator=g).to(dtype).cuda()
+    q_out = torch.empty((sum(lens), Hq, 128), dtype=dtype, device="cuda")
+    cache.extend(torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    cache.append(qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], q_out)
+    return cache, q_out, qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+
+
+class RawStream:
+    """Another library's stream object: only its handle."""
+
+    def __init__(self, s):
+        self.cuda_stream = s.cuda_stream
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_prune_and_gather_on_a_side_stream(raw):
+    """With the current stream busy: what prune allocates and clears has to be in the side stream's order, and memory
+    that it drops must not come back to the current stream's work before the side stream is done with it."""
+    cache, q, _, _ = filled([700, 300])
+    q_win = q[668:700].transpose(0, 1)[None].contiguous()
+    want, want_v = cache.prune(0, 700, q_win, 64)
+    want_k, _ = cache.gather(1, 300)
+    torch.cuda.synchronize()
+    current, side = torch.cuda.current_stream(), torch.cuda.Stream()
+    for _ in range(3):
+        dirt = [torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(40)]
+        del dirt
+        torch.cuda._sleep(20_000_000)  # about 10 ms
+        s = RawStream(side) if raw else side
+        got, v = cache.prune(0, 700, q_win, 64, stream=s)
+        k, _ = cache.gather(1, 300, stream=s)
+        later = [torch.full_like(k, 7.0) for _ in range(8)] + [torch.full_like(v, 7.0) for _ in range(8)]
+        side.synchronize()
+        assert torch.cuda.current_stream() == current
+        assert qdk.think_read_device_status(got.score_ws, side) == 0
+        with torch.cuda.stream(side):
+            assert torch.equal(got.idx, want.idx) and torch.equal(got.k_pruned[..., :700], want.k_pruned[..., :700])
+            assert torch.equal(v, want_v) and torch.equal(k, want_k)
+        del later
+    torch.cuda.synchronize()
+    side.wait_stream(current)
+    cache.release(0, stream=RawStream(side) if raw else side)
+    side.synchronize()
+    assert cache.kv_lens.tolist() == [0, 300] and cache.free_count.item() == 22 + 8
