@@ -749,12 +749,18 @@ class PagedCache:
                 think_gather_pages(cache, self.block_table[b:b + 1], self.kv_lens[b:b + 1], o)
         return out
 
-    def prune(self, b: int, N: int, q_win, T: int, layer: int = 0, stream=None):
+    def prune(self, b: int, N: int, q_win, T: int, layer: int = 0, stream=None, capacity: int | None = None):
         """Request b, N tokens long, pruned to T key channels by its window queries q_win [1,Hq,S,d]: a PrunedCache and
-        the values [1,Hkv,N,d] for its decode."""
+        the values for its decode.  To generate from it, give the `capacity` that both may grow to: the values are
+        then [1,Hkv,capacity,d], and a token's step is to write its values to row n, append its keys (as think_norm_rope_append
+        leaves them, not gathered) and decode."""
         with self._on(stream):
-            k, v = self.gather(b, N, layer)
-            pruned = PrunedCache(1, self.Hq, self.Hkv, N, T, self.d, dtype=self.dtype, device=k.device)
+            room = N if capacity is None else max(N, capacity)
+            k = torch.empty((1, self.Hkv, N, self.d), dtype=self.dtype, device=self.kv_lens.device)
+            v = torch.empty((1, self.Hkv, room, self.d), dtype=self.dtype, device=self.kv_lens.device)
+            for cache, o in ((self.k_cache[layer], k), (self.v_cache[layer], v)):
+                think_gather_pages(cache, self.block_table[b:b + 1], self.kv_lens[b:b + 1], o)
+            pruned = PrunedCache(1, self.Hq, self.Hkv, N, T, self.d, dtype=self.dtype, device=k.device, capacity=room)
             pruned.prune(q_win, k)
         return pruned, v
 

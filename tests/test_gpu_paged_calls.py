@@ -84,3 +84,33 @@ def test_prune_and_gather_on_a_side_stream(raw):
     cache.release(0, stream=RawStream(side) if raw else side)
     side.synchronize()
     assert cache.kv_lens.tolist() == [0, 300] and cache.free_count.item() == 22 + 8
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_generate_after_the_hand_over(dtype):
+    """A pruned prompt grows by more tokens than its rows are padded by, each decoded against the oracle."""
+    import oracle
+    from helpers import check_out
+    N, more, T, Hq, Hkv = 301, 13, 51, 8, 2
+    cache, q, k, v = filled([40, N + more], dtype=dtype, seed=7)
+    cache.kv_lens[1] = N  # the rest comes token by token
+    q_win = q[40 + N - 32:40 + N].transpose(0, 1)[None].contiguous()
+    pruned, values = cache.prune(1, N, q_win, T, capacity=N + more)
+    assert values.shape == (1, Hkv, N + more, 128) and not values[:, :, N:].any()
+    keys, _ = cache.gather(1, N)
+    f64 = lambda t: t.cpu().to(F64).numpy()
+    for i in range(more):
+        row = 40 + N + i
+        new = k[row].reshape(1, Hkv, 1, 128).contiguous()
+        keys = torch.cat([keys, new], 2)
+        values[:, :, pruned.n] = v[row]
+        pruned.append(new)
+        assert pruned.n == N + i + 1
+        out = torch.empty((1, Hq, 128), dtype=F32, device="cuda")
+        pruned.decode(q[row:row + 1], values, out)
+        idx = pruned.idx.cpu().numpy()
+        kp = f64(keys.gather(3, pruned.idx.long()[:, :, None].expand(-1, -1, pruned.n, -1)))
+        check_out(out, oracle.oracle_decode(f64(q[row:row + 1]), kp, f64(values[:, :, :pruned.n]), idx), dtype)
+    assert qdk.think_read_device_status(pruned.decode_ws) == 0
+    with pytest.raises(qdk.ThinkError):
+        pruned.append(torch.zeros((1, Hkv, 64, 128), dtype=dtype, device="cuda"))
