@@ -422,7 +422,13 @@ think_status_t think_gather_tokens(const void *x, const int64_t x_strides[3], in
  * THINK_DEVICE_NO_PAGES in the status word, if its tokens do not fit its table
  * row or the T rows, or if the pages wanted by it and the requests before it
  * (those that fit) exceed *free_count.  The slot of a page number below 0
- * (in the table or the stack) is -1, with THINK_DEVICE_BAD_PAGE.
+ * (in the table or the stack) is -1, with THINK_DEVICE_BAD_PAGE.  q_start counts
+ * the rows of such a request all the same: a row below q_start[B] with slot -1 is not
+ * in the cache.  think_norm_rope_append writes no key or value for it, and
+ * think_paged_attn, which knows lengths and row ranges only, takes the request's
+ * last tokens for the new ones: what it gives for these rows (numbers that look
+ * like others, no status bit) means nothing.  Hand the request's tokens in again
+ * once there is room.
  *   kv_lens_out may be kv_lens and free_count_out may be free_count; no other
  * buffers may overlap.  Without requests (B == 0) nothing is written.  workspace: think_extend_pages_workspace_size() bytes,
  * zeroed once (think_workspace_init); it holds the status word. */

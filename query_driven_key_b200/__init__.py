@@ -724,7 +724,8 @@ class PagedCache:
 
     def extend(self, new_lens, rows: int | None = None, stream=None):
         """new_lens [B] int32 new tokens of each request -> lengths, tables, positions and slots of this step's `rows`
-        rows (default: max_rows; rows behind the last request get slot -1)."""
+        rows (default: max_rows; rows behind the last request get slot -1).  A request that finds no room keeps its
+        length and its rows get slot -1 (status() tells): what attend gives for them means nothing."""
         self.positions, self.slots = (self._positions, self._slots) if rows is None else \
             (self._positions[:rows], self._slots[:rows])
         think_extend_pages(new_lens, self.kv_lens, self.block_table, self.free_pages, self.free_count, self.page_size,
@@ -740,6 +741,16 @@ class PagedCache:
         """Attention of this step's rows (after append) over their requests' pages."""
         think_paged_attn(q, self.k_cache[layer], self.v_cache[layer], self.block_table, self.q_start, self.kv_lens, out,
                          self.attn_ws, window, scale, max_new, stream)
+
+    def status(self, stream=None) -> int:
+        """The status bits (THINK_DEVICE_*) of the steps since the last call; waits for the stream.  After
+        THINK_DEVICE_NO_PAGES, rows below q_start[B] with slot -1 were not taken."""
+        with self._on(stream):
+            bits = [think_read_device_status(w) for w in (self.extend_ws, self.attn_ws)]
+            for w, x in zip((self.extend_ws, self.attn_ws), bits):
+                if x:
+                    think_workspace_init(w)
+        return bits[0] | bits[1]
 
     def gather(self, b: int, N: int, layer: int = 0, stream=None):
         """The first N tokens of request b, contiguous: k, v [1,Hkv,N,d]."""

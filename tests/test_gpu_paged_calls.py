@@ -1,8 +1,11 @@
 """Calls of the paged cache that meet other threads, streams, refusals and extreme values, on the GPU."""
+import math
 import threading
 
 import pytest
 import torch
+
+import paged_plain as P
 
 pytestmark = pytest.mark.gpu
 qdk = pytest.importorskip("query_driven_key_b200")
@@ -114,3 +117,46 @@ def test_generate_after_the_hand_over(dtype):
     assert qdk.think_read_device_status(pruned.decode_ws) == 0
     with pytest.raises(qdk.ThinkError):
         pruned.append(torch.zeros((1, Hkv, 64, 128), dtype=dtype, device="cuda"))
+
+
+def test_a_refused_request_beside_others_and_again():
+    """Three requests of which the second finds no pages: the others' rows are right, its own have slot -1 and the status
+    tells; nothing of it is in the cache, and its tokens go in when another request has left."""
+    Hq, Hkv, page = 4, 2, 16
+    cache = qdk.PagedCache(3, Hq, Hkv, num_pages=7, page_size=page, max_blocks=8, max_rows=128)
+    g = torch.Generator().manual_seed(2)
+
+    def step(new):
+        T = sum(new)
+        qkv = torch.randn((T, Hq + 2 * Hkv, 128), generator=g).to(BF)
+        dev = qkv.cuda()
+        q_out, out = (torch.full((T, Hq, 128), 9.0, dtype=BF, device="cuda") for _ in range(2))
+        cache.extend(torch.tensor(new, dtype=torch.int32, device="cuda"), rows=T)
+        cache.append(dev[:, :Hq], dev[:, Hq:Hq + Hkv], dev[:, Hq + Hkv:], q_out)
+        cache.attend(q_out, out)
+        return qkv, out.cpu()
+
+    def check(qkv, out, requests):
+        starts = cache.q_start.tolist()
+        want, size, logit = P.attend(qkv[:, :Hq], cache.k_cache[0].cpu(), cache.v_cache[0].cpu(), cache.block_table.tolist(),
+                                     starts, [n if b in requests else 0 for b, n in enumerate(cache.kv_lens.tolist())], 0,
+                                     1 / math.sqrt(128))
+        limit = P.attend_bound(want, size, logit, BF, 128)
+        for b in requests:
+            rows = slice(starts[b], starts[b + 1])
+            assert ((out[rows].to(F64) - want[rows]).abs() <= limit[rows]).all()
+
+    check(*step([40, 20, 10]), (0, 1, 2))  # 3, 2 and 1 pages
+    assert cache.status() == 0
+    before = [c.clone() for c in (cache.k_cache[0], cache.v_cache[0], cache.block_table, cache.free_count)]
+    qkv, out = step([4, 30, 1])            # the second wants 2 pages of 1
+    assert cache.kv_lens.tolist() == [44, 20, 11] and cache.q_start.tolist() == [0, 4, 34, 35]
+    assert (cache.slots[4:34] == -1).all() and (cache.slots[:4] >= 0).all() and (cache.slots[34:] >= 0).all()
+    check(qkv, out, (0, 2))
+    assert torch.equal(before[2], cache.block_table) and torch.equal(before[3], cache.free_count)
+    written = (cache.k_cache[0] != before[0]).any(-1).sum().item()
+    assert written == 5 * Hkv
+    assert cache.status() == qdk.THINK_DEVICE_NO_PAGES and cache.status() == 0
+    cache.release(2)
+    check(*step([0, 30, 0]), (1,))
+    assert cache.kv_lens.tolist() == [44, 50, 0] and cache.status() == 0
