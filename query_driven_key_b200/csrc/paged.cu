@@ -120,18 +120,18 @@ think_status_t launch_paged_tc32(const PagedArgs &a, cudaStream_t st)
     return launch_pdl(paged_tc32_kernel, dim3(kTargetSMs), dim3(kP32Threads), kP32Smem, st, a);
 }
 
-template <typename T, bool NEIGHBOURS, int SLOTS, bool SHARED>
+template <typename T, bool NEIGHBOURS, bool ALL, int SLOTS, bool SHARED>
 think_status_t launch_rope_s(const RopeArgs &a, int64_t shares, int64_t blocks, cudaStream_t st)
 {
     const int groups = kRopeThreads * 16 / (kD * (int)sizeof(T));
     const int64_t rows = ceil_div(a.Hq + 2 * (int64_t)a.Hkv, shares) * a.unit;
     const size_t smem = (size_t)kRopeStages * (size_t)ceil_div(rows, groups) * kRopeThreads * 16;
-    auto kern = norm_rope_append_kernel<T, NEIGHBOURS, SLOTS, SHARED>;
+    auto kern = norm_rope_append_kernel<T, NEIGHBOURS, ALL, SLOTS, SHARED>;
     if (!ensure_smem(reinterpret_cast<const void *>(kern), smem)) return THINK_ERR_CUDA;
     return launch_pdl(kern, dim3((unsigned)blocks, (unsigned)shares), dim3(kRopeThreads), smem, st, a);
 }
 
-template <typename T, bool NEIGHBOURS>
+template <typename T, bool NEIGHBOURS, bool ALL>
 think_status_t launch_rope_n(RopeArgs a, cudaStream_t st)
 {
     // A group of 16 (bf16) or 32 (fp32) lanes takes up to three head rows of a token, and blocks share the heads so
@@ -151,15 +151,16 @@ think_status_t launch_rope_n(RopeArgs a, cudaStream_t st)
     for (int u = 2; u <= kRopeBatch && places(u) <= 2 && u * most <= a.T; u *= 2)
         if (u * places(a.unit) > a.unit * places(u)) a.unit = u;
     const int64_t blocks = std::min(a.T, most);
-    if (a.unit > 1) return launch_rope_s<T, NEIGHBOURS, 2, true>(a, shares, blocks, st);
-    if (ceil_div(heads, shares) > 2 * groups) return launch_rope_s<T, NEIGHBOURS, 3, false>(a, shares, blocks, st);
-    return launch_rope_s<T, NEIGHBOURS, 2, false>(a, shares, blocks, st);
+    if (a.unit > 1) return launch_rope_s<T, NEIGHBOURS, ALL, 2, true>(a, shares, blocks, st);
+    if (ceil_div(heads, shares) > 2 * groups) return launch_rope_s<T, NEIGHBOURS, ALL, 3, false>(a, shares, blocks, st);
+    return launch_rope_s<T, NEIGHBOURS, ALL, 2, false>(a, shares, blocks, st);
 }
 
 template <typename T>
 think_status_t launch_rope(bool neighbours, const RopeArgs &a, cudaStream_t st)
 {
-    return neighbours ? launch_rope_n<T, true>(a, st) : launch_rope_n<T, false>(a, st);
+    if (a.rot == kD) return neighbours ? launch_rope_n<T, true, true>(a, st) : launch_rope_n<T, false, true>(a, st);
+    return neighbours ? launch_rope_n<T, true, false>(a, st) : launch_rope_n<T, false, false>(a, st);
 }
 
 }  // namespace

@@ -21,7 +21,7 @@
 // at position 131072 an fp32 product is off by up to 2^-24 * 131072 = 0.008 rad.
 // All arithmetic after it is fp32, with one rounding at the store.
 // Measured: 8192 tokens of 32 + 8 + 8 bf16 heads (201 MB) 42.1 us = 4.8 TB/s;
-// 1777 tokens of 12 + 4 + 4 fp32 heads (36 MB) 8.4 us; one token 3.5 us.  Bound by
+// 1777 tokens of 12 + 4 + 4 fp32 heads (36 MB) 8.5 us; one token 3.5 us.  Bound by
 // the issue of instructions (147 for two rows of a warp, 0.64 of the issue slots)
 // beside HBM: what helps is fewer idle lanes.  512 threads of two rows each 43.3
 // (48 rows are one and a half a thread group); rows held in registers instead
@@ -127,7 +127,9 @@ template <> struct RopeChunk<float> {
 // SHARED: few heads; a step takes a.unit tokens (else one), whose rows, one after
 // another, fill the row slots (8192 tokens of 1 + 1 + 1 bf16 heads 10.9 us, a token a
 // step 22.7).
-template <typename T, bool NEIGHBOURS, int SLOTS, bool SHARED>
+// ALL: every channel is turned (rot == 128); looking whether a lane's are costs 2% (8192
+// tokens of 48 heads 42.2 -> 43.2 us).
+template <typename T, bool NEIGHBOURS, bool ALL, int SLOTS, bool SHARED>
 __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSM) norm_rope_append_kernel(const RopeArgs a)
 {
     constexpr int CH = RopeChunk<T>::N;           // channels of a chunk
@@ -291,12 +293,17 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocksPerSM) norm_rope_appe
 #pragma unroll
                 for (int j = 0; j < VEC / 2; ++j) f4[j] = s_f[k][kind[i]][j][lane];
                 const uint64_t *f = reinterpret_cast<const uint64_t *>(f4);  // cos w: P + P pairs, sin w': P + P
+                if (ALL || a0 < a.rot) {
 #pragma unroll
-                for (int j = 0; j < P; ++j) {
-                    const uint64_t px = NEIGHBOURS ? swap2(x[j]) : z[j], pz = NEIGHBOURS ? swap2(z[j]) : x[j];
-                    const uint64_t y = fma2(px, f[2 * P + j], mul2(x[j], f[j]));
-                    z[j] = mul2(fma2(pz, f[3 * P + j], mul2(z[j], f[P + j])), inv2);
-                    x[j] = mul2(y, inv2);
+                    for (int j = 0; j < P; ++j) {
+                        const uint64_t px = NEIGHBOURS ? swap2(x[j]) : z[j], pz = NEIGHBOURS ? swap2(z[j]) : x[j];
+                        const uint64_t y = fma2(px, f[2 * P + j], mul2(x[j], f[j]));
+                        z[j] = mul2(fma2(pz, f[3 * P + j], mul2(z[j], f[P + j])), inv2);
+                        x[j] = mul2(y, inv2);
+                    }
+                } else {  // no partners (an infinity times a sine of 0 would be NaN)
+#pragma unroll
+                    for (int j = 0; j < P; ++j) x[j] = mul2(mul2(x[j], f[j]), inv2), z[j] = mul2(mul2(z[j], f[P + j]), inv2);
                 }
                 const int64_t off = s_off[k][kind[i]];
                 if (off >= 0) {

@@ -160,3 +160,36 @@ def test_a_refused_request_beside_others_and_again():
     cache.release(2)
     check(*step([0, 30, 0]), (1,))
     assert cache.kv_lens.tolist() == [44, 50, 0] and cache.status() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("neighbours", [False, True])
+@pytest.mark.parametrize("rot", [0, 32, 96, 128])
+@pytest.mark.parametrize("T,Hq,Hkv", [(3, 2, 1), (40, 40, 4), (2600, 1, 1)])
+def test_infinities_stay_in_their_channels(T, Hq, Hkv, rot, neighbours, dtype):
+    """Without a norm, channels that are not turned are copied bit for bit, infinities and NaN among them, and a turned pair
+    is spoilt by its own two channels alone."""
+    g = torch.Generator().manual_seed(rot + T)
+    qkv = torch.randn((T, Hq + 2 * Hkv, 128), generator=g).to(dtype)
+    hit = torch.rand(qkv.shape, generator=g) < 0.05
+    odd = torch.tensor([math.inf, -math.inf, math.nan, -0.0])[torch.randint(0, 4, qkv.shape, generator=g)]
+    qkv = torch.where(hit, odd, qkv).to(dtype)
+    dev = qkv.cuda()
+    freq = None if rot == 0 else (100.0 ** (-torch.arange(0, rot, 2, dtype=F64) / rot)).cuda()
+    pos = torch.randint(1, 1000, (T,), generator=g).to(torch.int32)
+    pages = -(-T // 16)
+    kc, vc = (torch.zeros((pages, Hkv, 16, 128), dtype=dtype, device="cuda") for _ in range(2))
+    q_out = torch.zeros((T, Hq, 128), dtype=dtype, device="cuda")
+    qdk.think_norm_rope_append(dev[:, :Hq], dev[:, Hq:Hq + Hkv], dev[:, Hq + Hkv:], None, None, 0.0, freq, neighbours,
+                               pos.cuda(), torch.arange(T, device="cuda"), q_out, kc, vc)
+    rows = lambda c: c.cpu().transpose(1, 2).reshape(-1, Hkv, 128)[:T]
+    bits = lambda t: t.contiguous().view(torch.int16 if dtype == BF else torch.int32)
+    got = torch.cat([q_out.cpu(), rows(kc)], 1)
+    x = qkv[:, :Hq + Hkv]
+    same = (bits(got[..., rot:]) == bits(x[..., rot:])) | (got[..., rot:].isnan() & x[..., rot:].isnan())
+    assert same.all()
+    assert torch.equal(bits(rows(vc)), bits(qkv[:, Hq + Hkv:]))
+    for i in range(rot // 2):
+        a, b = (2 * i, 2 * i + 1) if neighbours else (i, i + rot // 2)
+        fine = x[..., a].isfinite() & x[..., b].isfinite()
+        assert (got[..., a].isfinite() == fine).all() and (got[..., b].isfinite() == fine).all()
