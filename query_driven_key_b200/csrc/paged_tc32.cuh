@@ -59,12 +59,23 @@ struct P32Bars {
     uint32_t abort_flag;
 };
 
-// The three parts of two numbers, each as a pair of bf16.
+// Two numbers as a pair of bf16, the largest bf16 number in place of one that would
+// round to infinity.
+__device__ __forceinline__ uint32_t bf16_pair_finite(float lo, float hi)
+{
+    uint32_t d;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+
+// The three parts of two numbers, each as a pair of bf16.  (fp32 numbers beyond the
+// largest bf16 one leave a remainder for the second part like others; an
+// infinity leaves infinities, and NaN as the third part.)
 __device__ __forceinline__ void split3(float a, float b, uint32_t (&w)[3])
 {
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
-        w[p] = bf16_pair(a, b);
+        w[p] = p == 0 ? bf16_pair_finite(a, b) : bf16_pair(a, b);
         a -= bf16lo(w[p]);
         b -= bf16hi(w[p]);
     }

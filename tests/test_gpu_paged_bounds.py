@@ -94,3 +94,25 @@ def test_fp32_logits_keep_their_third_parts():
     got = attend(qq, k, v, [[b] for b in range(B)], list(range(B + 1)), [2] * B, scale=1.0).cpu().to(F64)
     want, limit = Q.two_key_want(q, k0), Q.two_key_bound(q, k0)
     assert ((got[:, 0] - want[:, None]).abs() / limit[:, None]).max().item() <= 1.0
+
+
+def test_fp32_numbers_beyond_the_largest_bf16_one():
+    """Finite numbers that round to infinity in bf16, as values and as keys; infinite values spoil their channel alone."""
+    top = torch.finfo(F32).max
+    v = torch.zeros(1, 1, 16, 128)
+    v[0, 0, 0] = top * (1 - torch.arange(128) * 2.0 ** -14)
+    v[0, 0, 0, 64:] *= -1
+    got = attend(torch.randn(1, 1, 128), torch.randn(1, 1, 16, 128), v, [[0]], [0, 1], [1]).cpu().to(F64)
+    want = v[0, 0, 0].to(F64)
+    assert ((got[0, 0] - want) / want).abs().max().item() <= Q.mean_bound(1)
+    v[0, 0, 0, 7], v[0, 0, 0, 70] = math.inf, -math.inf
+    got = attend(torch.randn(1, 1, 128), torch.randn(1, 1, 16, 128), v, [[0]], [0, 1], [1]).cpu()
+    fine = torch.ones(128, dtype=torch.bool)
+    fine[[7, 70]] = False
+    assert (got[0, 0].isfinite() == fine).all()
+    q, k, v = torch.zeros(2, 1, 128), torch.zeros(2, 1, 16, 128), torch.zeros(2, 1, 16, 128)
+    q[:, 0, 5], k[:, 0, 0, 5] = torch.tensor([2.0 ** -126, -(2.0 ** -126)]), torch.tensor([top, -top])
+    v[:, 0, 0], v[:, 0, 1] = 1.0, -1.0
+    got = attend(q, k, v, [[0], [1]], [0, 1, 2], [2, 2], scale=1.0).cpu().to(F64)
+    a, b = q[:, 0, 5].abs(), k[:, 0, 0, 5].abs()
+    assert ((got[:, 0] - Q.two_key_want(a, b)[:, None]).abs() <= Q.two_key_bound(a, b)[:, None]).all()
