@@ -146,20 +146,29 @@ def _load() -> ctypes.CDLL:
 lib = _load()
 
 
-def _load_binding():
-    """The module that marshals the paged calls, bound to the loaded library's entry points."""
-    path = os.path.join(_PKG, "_binding.so")
-    if not os.path.exists(path):
-        raise ImportError(f"_binding.so not found at {path}; build it with `python query_driven_key_b200/build.py`")
-    spec = importlib.util.spec_from_file_location("query_driven_key_b200._binding", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
-    module.bind(*(ctypes.cast(getattr(lib, "think_" + f), ctypes.c_void_p).value
-                  for f in ("extend_pages", "norm_rope_append", "paged_attn", "gather_pages")))
-    return module
+class _Binding:
+    """The module that marshals the paged calls, bound to the loaded library's entry points.  It is loaded by the first
+    of them: the other calls need only libthink.so, and work where it is missing."""
+
+    def __getattr__(self, name: str):
+        if name.startswith("__"):
+            raise AttributeError(name)
+        path = os.path.join(_PKG, "_binding.so")
+        if not os.path.exists(path):
+            raise ImportError(f"_binding.so not found at {path}; build it with `python query_driven_key_b200/build.py`")
+        spec = importlib.util.spec_from_file_location("query_driven_key_b200._binding", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        if module.torch_version != torch.__version__:
+            raise ImportError(f"_binding.so was built with torch {module.torch_version}, this is {torch.__version__}; "
+                              "build it again with `python query_driven_key_b200/build.py`")
+        module.bind(*(ctypes.cast(getattr(lib, "think_" + f), ctypes.c_void_p).value
+                      for f in ("extend_pages", "norm_rope_append", "paged_attn", "gather_pages")))
+        globals()["_binding"] = module
+        return getattr(module, name)
 
 
-_binding = _load_binding()
+_binding = _Binding()
 
 
 class ThinkError(RuntimeError):

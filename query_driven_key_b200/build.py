@@ -57,16 +57,23 @@ def _build_one(lib: str, flags, force: bool, verbose: bool) -> str:
     return lib
 
 
-def _build_binding(force: bool, verbose: bool) -> str:
+def _binding_is_current(version: str) -> bool:
     deps = [BINDING_SRC, os.path.join(INCLUDE, "think.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= max(map(os.path.getmtime, deps)):
-        return BINDING
+    if not os.path.exists(BINDING) or os.path.getmtime(BINDING) < max(map(os.path.getmtime, deps)):
+        return False
+    with open(BINDING, "rb") as f:
+        return f"torch_version={version}\0".encode() in f.read()
+
+
+def _build_binding(force: bool, verbose: bool) -> str:
     import torch
+    if not force and _binding_is_current(torch.__version__):
+        return BINDING
     troot = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     tmp = BINDING + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-I", INCLUDE, "-isystem", os.path.join(troot, "include"),
+           f'-DTHINK_TORCH_VERSION="{torch.__version__}"', "-I", INCLUDE, "-isystem", os.path.join(troot, "include"),
            "-isystem", os.path.join(troot, "include", "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], "-isystem", os.path.join(cuda, "include"), BINDING_SRC,
            "-L", os.path.join(troot, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-o", tmp]

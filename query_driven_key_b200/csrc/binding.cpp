@@ -308,4 +308,16 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+// The torch that this was built with: its C++ interface is not stable between
+// versions.  (The build looks for the text, so as to build again for another one.)
+const char kTorchVersion[] = "torch_version=" THINK_TORCH_VERSION;
+
+PyMODINIT_FUNC PyInit__binding()
+{
+    PyObject *m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "torch_version", std::strchr(kTorchVersion, '=') + 1) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
