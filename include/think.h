@@ -450,7 +450,8 @@ think_status_t think_extend_pages(const int32_t *new_lens, const int32_t *kv_len
  * must differ from one another.
  *   q [T][Hq][d], k, v [T][Hkv][d], q_out [T][Hq][d]: strides of the token and
  *   the head in elements (they may be views of one projection's output).
- *   q_out may be q itself (same address and strides), else buffers may not overlap.
+ *   q_out may be q itself (same address and strides), else buffers may not overlap;
+ *   q_out and the caches have no stride of 0 (of more than one element).
  *   q_weight, k_weight: [d] of dtype, or NULL for no norm.  eps >= 0.
  *   inv_freq: [rot/2] fp64 device array (NULL if rot == 0); rot a multiple of
  *   16, at most d.  Hq or Hkv may be 0. */
@@ -471,7 +472,8 @@ think_status_t think_norm_rope_append(const void *q, const int64_t q_strides[2],
  * for each query head h, over KV head h / G; a row that sees no key (p < 0)
  * gets zeros.  Arithmetic: fp32 sums and softmax; bf16 rounds the softmax
  * weights to bf16 before the product with V, as it rounds the output.
- *   q, out   [T][Hq][d] of dtype, strides of the token and the head.  Rows
+ *   q, out   [T][Hq][d] of dtype, strides of the token and the head (of out not 0
+ *            where there is more than one).  Rows
  *            outside every request's range are not written.  out may not overlap
  *            q or the caches.
  *   max_new  the largest number of new tokens of a request, or 0 if not

@@ -7,6 +7,7 @@
 #include <climits>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 #include <numeric>
 
 #include "host.cuh"
@@ -33,6 +34,15 @@ inline bool strides16(const int64_t *s, int n, size_t es)
 {
     for (int i = 0; i < n; ++i)
         if (s[i] < 0 || s[i] % (int64_t)(16 / es) != 0) return false;
+    return true;
+}
+
+// Rows that a call writes: no stride of 0 along a dimension of more than one element
+// (several rows would be written to one place, in no order).
+inline bool apart(const int64_t *s, std::initializer_list<int64_t> sizes)
+{
+    for (const int64_t n : sizes)
+        if (*s++ == 0 && n > 1) return false;
     return true;
 }
 
@@ -108,7 +118,7 @@ think_status_t launch_paged_tc(const PagedArgs &a, cudaStream_t st)
         return THINK_ERR_CUDA;
     // the most key tiles of an item that a block can have: an item's, or an equal share of all items' and what is not cut
     const int64_t tiles = ceil_div(a.limit, kPtBN), items = a.Hkv * (ceil_div((int64_t)a.T * G, kPtRows) + a.B);
-    const bool is_long = std::min(tiles, items * (tiles + kItemCost<kPtRows>) / kTargetSMs + 17) > kPtFold;
+    const bool is_long = std::min(tiles, std::min<int64_t>(items, INT32_MAX) * (tiles + kItemCost<kPtRows>) / kTargetSMs + 17) > kPtFold;
     const auto kern = is_long ? paged_tc_kernel<true> : paged_tc_kernel<false>;
     if (!ensure_smem(reinterpret_cast<const void *>(kern), paged_tc_smem())) return THINK_ERR_CUDA;
     return launch_pdl(kern, dim3(kTargetSMs), dim3(kPtThreads), paged_tc_smem(), st, mk, mv, mq, a, ks.outer(), vs.outer(), chunk, tma_q);
@@ -248,6 +258,9 @@ think_status_t think_norm_rope_append(const void *q, const int64_t q_strides[2],
         (Hkv > 0 && (!strides16(k_strides, 2, es) || !strides16(v_strides, 2, es) || !strides16(k_cache_strides, 3, es) ||
                      !strides16(v_cache_strides, 3, es))))
         return THINK_ERR_ALIGNMENT;
+    if ((Hq > 0 && !apart(q_out_strides, {T, Hq})) ||
+        (Hkv > 0 && (!apart(k_cache_strides, {num_pages, Hkv, page_size}) || !apart(v_cache_strides, {num_pages, Hkv, page_size}))))
+        return THINK_ERR_INVALID_ARG;
     RopeArgs a = {};
     a.q = q, a.k = k, a.v = v, a.wq = q_weight, a.wk = k_weight;
     a.q_out = q_out, a.k_cache = k_cache, a.v_cache = v_cache;
@@ -297,6 +310,7 @@ think_status_t think_paged_attn(const void *q, const int64_t q_strides[2], const
         !aligned4(q_start) || !aligned4(kv_lens) || !strides16(q_strides, 2, es) || !strides16(out_strides, 2, es) ||
         !strides16(k_cache_strides, 3, es) || !strides16(v_cache_strides, 3, es))
         return THINK_ERR_ALIGNMENT;
+    if (!apart(out_strides, {T, Hq})) return THINK_ERR_INVALID_ARG;
     for (const int64_t *c : {k_cache_strides, v_cache_strides})  // TMA: strides (eight rows' too) above 0 and below 2^40 bytes
         for (int i = 0; i < 3; ++i) {
             if (c[i] == 0 && (i == 0 ? num_pages : i == 1 ? Hkv : page_size) > 1) return THINK_ERR_INVALID_ARG;
