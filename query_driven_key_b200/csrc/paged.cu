@@ -146,7 +146,7 @@ think_status_t launch_rope_n(RopeArgs a, cudaStream_t st)
 {
     // A group of 16 (bf16) or 32 (fp32) lanes takes up to three head rows of a token, and blocks share the heads so
     // that a block's tokens times (its rows a group, and a half for the factors, which each forms) are fewest: three
-    // for many tokens (8192 of 48 bf16 heads: 41.5 us, two 43.7), one for few, which are then spread over the blocks.
+    // for many tokens (8192 of 48 bf16 heads: 42.1 us, two 43.7), one for few, which are then spread over the blocks.
     // With few heads and many tokens a step takes as many tokens as fill one place, or two.
     const int groups = kRopeThreads * 16 / (kD * (int)sizeof(T));
     const int64_t heads = a.Hq + 2 * (int64_t)a.Hkv;

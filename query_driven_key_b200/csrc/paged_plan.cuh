@@ -154,7 +154,9 @@ struct PlanSmem {
 // half the time; an fp32 tile takes as long as a join.)  Measured, cut -> whole: 16
 // single tokens over 250 to 500 keys 29.0 -> 14.6 us, over 1000 to 2000 39.0 -> 34.2,
 // 64 over 500 to 1000 67.0 -> 58.8; a prompt of 400 tokens 26.7 -> 15.4, of 1000 37.2
-// -> 24.2.  Up to 24 tiles whole: one token over 4000 keys 18 -> 26.
+// -> 24.2.  Where whole items are fewer than the blocks it is not slower either (single
+// calls between events, which add about 10 us, 8 heads): one request of 1000 keys
+// 29.7 -> 23.6, of 2000 30.8 -> 30.7, 4 of 2000 31.7 both ways.
 template <int R>
 __device__ __forceinline__ int uncut(int rows)
 {

@@ -31,9 +31,11 @@
 // the page holds), 1 for the products.  Shared memory holds one tile of keys
 // and one of values (48 KB each with their parts) beside the queries (96 KB);
 // logits have two buffers in TMEM, so that the next tile's run beside this one's
-// softmax.  Bound by the products: 72 a tile, about 4100 cycles, and by a tile's
-// chain from logits to O, which only the next tile's logits overlap.  Measured:
-// 3 chunks of 90 to 400 tokens over up to 2900 keys, 8 heads (1.5 GFLOP) 52 us;
+// softmax.  Long items are bound by the products, 72 a tile, about 4100 cycles, whatever
+// the rows (131072 keys of 8 heads, one token: 436 us, where HBM would take 166); short
+// ones by an item's start and end, a tile's chain from logits to O, which only the
+// next tile's logits overlap, and joins (the tensor pipe is active 17% of the chunks' time).  Measured:
+// 3 chunks of 90 to 400 tokens over up to 2900 keys, 8 heads (1.5 GFLOP) 52.7 us;
 // on the FMA pipes with cp.async 102, and 61 without warps of their own for the
 // keys' and the values' parts.
 // Every wait is bounded, as in the bf16 kernel.
