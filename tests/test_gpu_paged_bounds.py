@@ -18,7 +18,8 @@ def attend(q, k, v, table, q_start, lens, window=0, scale=SCALE):
     i32 = lambda x: torch.as_tensor(x, dtype=torch.int32).cuda()
     q, k, v = q.cuda(), k.cuda(), v.cuda()
     T, Hq, _ = q.shape
-    w = torch.zeros(qdk.think_paged_attn_workspace_size(T, Hq, k.shape[1], dtype=q.dtype), dtype=torch.uint8, device="cuda")
+    w = torch.full((qdk.think_paged_attn_workspace_size(T, Hq, k.shape[1], dtype=q.dtype),), 255, dtype=torch.uint8, device="cuda")
+    w[:256 + 2048] = 0  # (only the status word and the counters have to be zero: the scratch holds NaN)
     out = torch.full_like(q, 9.0)
     qdk.think_paged_attn(q, k, v, i32(table), i32(q_start), i32(lens), out, w, window=window, scale=scale)
     assert qdk.think_read_device_status(w) == 0
