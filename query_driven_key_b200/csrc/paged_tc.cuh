@@ -542,6 +542,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         if (real && !to_end) y[c * a.rows_cap] = __uint_as_float(o[c]);
                         if (!to_end) o[c] = 0u;
                     }
+                    __syncwarp();
                     tc05::tmem_st8(o_addr + 8u * i, o);
                 }
                 tc05::tmem_st_wait();

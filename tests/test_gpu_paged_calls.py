@@ -193,3 +193,32 @@ def test_infinities_stay_in_their_channels(T, Hq, Hkv, rot, neighbours, dtype):
         a, b = (2 * i, 2 * i + 1) if neighbours else (i, i + rot // 2)
         fine = x[..., a].isfinite() & x[..., b].isfinite()
         assert (got[..., a].isfinite() == fine).all() and (got[..., b].isfinite() == fine).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_pool_of_more_than_2_to_the_32_elements(dtype):
+    """The last pages of pools whose offsets pass 32 bits: written, attended over and gathered like those of a small pool."""
+    Hq, Hkv, page, pages, n = 4, 2, 64, 300_000, 150
+    g = torch.Generator().manual_seed(8)
+    x = torch.randn((n, Hq + 2 * Hkv, 128), generator=g).to(dtype).cuda()
+    freq = (10000.0 ** (-torch.arange(0, 128, 2, dtype=F64) / 128)).cuda()
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    lens, rows = torch.tensor([n], dtype=torch.int32, device="cuda"), torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    results = []
+    for total in (3, pages):
+        kc, vc = (torch.empty((total, Hkv, page, 128), dtype=dtype, device="cuda") for _ in range(2))
+        table = torch.tensor([[total - 1, total - 3, total - 2]], dtype=torch.int32, device="cuda")
+        slots = table[0, pos.long() // page].long() * page + pos.long() % page
+        q_out, out = torch.empty_like(x[:, :Hq]), torch.empty((n, Hq, 128), dtype=dtype, device="cuda")
+        qdk.think_norm_rope_append(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], None, None, 0.0, freq, False, pos, slots, q_out, kc, vc)
+        w = torch.zeros(qdk.think_paged_attn_workspace_size(n, Hq, Hkv, dtype=dtype), dtype=torch.uint8, device="cuda")
+        qdk.think_paged_attn(q_out, kc, vc, table, rows, lens, out, w)
+        assert qdk.think_read_device_status(w) == 0
+        keys = torch.empty((1, Hkv, n, 128), dtype=dtype, device="cuda")
+        qdk.think_gather_pages(kc, table, lens, keys)
+        results.append((out, keys, vc[-1].clone()))
+        del kc, vc
+    assert pages * Hkv * page * 128 > 2 ** 32 and results[0][0].isfinite().all()
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    torch.cuda.empty_cache()
